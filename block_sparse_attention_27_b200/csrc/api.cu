@@ -35,8 +35,9 @@ int num_sms_current() {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Validates dims; fills Shape.  Returns DSA_OK or an error code.
-int make_shape(const dsa_dims *dims, Shape *out) {
+// Validates dims; fills Shape.  Returns DSA_OK or an error code.  any_block: the
+// block may be longer than 256 query rows per KV head.
+int make_shape(const dsa_dims *dims, Shape *out, bool any_block = false) {
   if (!dims) return DSA_ERR_INVALID_ARG;
   const dsa_dims &d = *dims;
   if (d.S <= 0 || d.B <= 0 || d.Hq <= 0 || d.Hkv <= 0 || d.d <= 0 || d.page <= 0 ||
@@ -46,7 +47,10 @@ int make_shape(const dsa_dims *dims, Shape *out) {
   if (d.d != 64 && d.d != 128) return DSA_ERR_UNSUPPORTED;
   if (d.page != 16 && d.page != 32 && d.page != 64) return DSA_ERR_UNSUPPORTED;
   const int G = d.Hq / d.Hkv;
-  if ((long long)d.B * G > 256) return DSA_ERR_UNSUPPORTED;
+  if (!any_block && (long long)d.B * G > 256) return DSA_ERR_UNSUPPORTED;
+  if (any_block && ((long long)d.S * d.B > INT32_MAX ||
+                    (long long)d.S * d.B > INT32_MAX / ((long long)d.Hq + 2LL * d.Hkv)))
+    return DSA_ERR_UNSUPPORTED;
   if ((long long)d.max_pages * d.page > (1LL << 30)) return DSA_ERR_UNSUPPORTED;
   if (d.sm_limit < 0) return DSA_ERR_INVALID_ARG;
   if (d.head_budget != 0 && d.head_budget != 1) return DSA_ERR_INVALID_ARG;
@@ -79,6 +83,27 @@ int select_sms(const Shape &sh) {
 template <class T>
 T *at(void *ws, size_t off) {
   return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
+}
+
+const __nv_bfloat16 *bf(const void *p) { return static_cast<const __nv_bfloat16 *>(p); }
+__nv_bfloat16 *bf(void *p) { return static_cast<__nv_bfloat16 *>(p); }
+
+bool good_window(const dsa_window *w) {
+  return w && w->window >= 1 && w->sinks >= 0 && (w->causal == 0 || w->causal == 1);
+}
+
+// The 4-bit cache's pointers; false if one is null or misaligned.
+bool make_kv4(const dsa_kv4 *c, dsa::Kv4 *out) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return false;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return false;
+  *out = dsa::Kv4{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), bf(c->k_scale), bf(c->v_scale)};
+  return true;
+}
+
+// Status workspace of the operators that need nothing else.
+int check_header(const void *workspace, size_t ws_bytes) {
+  if (!workspace || !aligned16(workspace)) return DSA_ERR_INVALID_ARG;
+  return ws_bytes < dsa::kWorkspaceHeader ? DSA_ERR_WORKSPACE_TOO_SMALL : DSA_OK;
 }
 
 }  // namespace
@@ -118,6 +143,9 @@ int dsa_kernels_per_call(int pass) {
   if (pass == 0) return dsa::kSelectLaunches;
   if (pass == 1) return dsa::kSparseLaunches;
   if (pass == 2) return dsa::kMergeLaunches;
+  if (pass == 3) return dsa::kRopeLaunches;
+  if (pass == 4) return dsa::kKv4StoreLaunches;
+  if (pass == 5) return dsa::kKv4LoadLaunches;
   return DSA_ERR_INVALID_ARG;
 }
 
@@ -318,6 +346,169 @@ int dsa_sparse_attn(const void *q_blk, const void *k_cache, const void *v_cache,
   a.status = at<uint32_t>(workspace, 0);
   a.xchg = at<unsigned char>(workspace, plan.off_xchg);
   if (dsa::launch_sparse(sh, plan, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+int dsa_qk_norm_rope(const void *q, const void *k, const void *v, void *q_out, void *k_out,
+                     void *v_out, void *k_cache, void *v_cache, dsa_stream_t stream,
+                     const dsa_dims *dims, const dsa_rope *rope, const int32_t *n_ctx,
+                     void *workspace, size_t ws_bytes) {
+  Shape sh;
+  int rc = make_shape(dims, &sh, true);
+  if (rc != DSA_OK) return rc;
+  if (!rope || !rope->inv_freq || (rope->interleaved != 0 && rope->interleaved != 1)) return DSA_ERR_INVALID_ARG;
+  if (rope->rot < 8 || rope->rot > sh.d || rope->rot % 8 != 0) return DSA_ERR_UNSUPPORTED;
+  if (!(rope->eps > 0.f) || !std::isfinite(rope->eps) || !std::isfinite(rope->scale)) return DSA_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_out != nullptr) || (k != nullptr) != (k_out || k_cache) ||
+      (v != nullptr) != (v_out || v_cache) || (!q && !k && !v))
+    return DSA_ERR_INVALID_ARG;
+  const bool appends = k_cache || v_cache;
+  if (!n_ctx && (appends || !rope->positions)) return DSA_ERR_INVALID_ARG;
+  for (const void *p : {q, k, v, (const void *)q_out, (const void *)k_out, (const void *)v_out,
+                        (const void *)k_cache, (const void *)v_cache, rope->q_norm, rope->k_norm})
+    if (!aligned16(p)) return DSA_ERR_INVALID_ARG;
+  const long long hq = (long long)sh.Hq * sh.d, hkv = (long long)sh.Hkv * sh.d;
+  auto bad_stride = [](int64_t st, long long least) { return st < least || st % 8 != 0; };
+  if ((q && bad_stride(rope->q_stride, hq)) || (k && bad_stride(rope->k_stride, hkv)) ||
+      (v && bad_stride(rope->v_stride, hkv)))
+    return DSA_ERR_INVALID_ARG;
+  if ((q && q == q_out && rope->q_stride != hq) || (k && k == k_out && rope->k_stride != hkv) ||
+      (v && v == v_out && rope->v_stride != hkv))
+    return DSA_ERR_INVALID_ARG;
+  rc = check_header(workspace, ws_bytes);
+  if (rc != DSA_OK) return rc;
+  dsa::RopeArgs a{};
+  a.q = bf(q); a.k = bf(k); a.v = bf(v);
+  a.q_out = bf(q_out); a.k_out = bf(k_out); a.v_out = bf(v_out);
+  a.k_cache = bf(k_cache); a.v_cache = bf(v_cache);
+  a.q_norm = bf(rope->q_norm); a.k_norm = bf(rope->k_norm);
+  a.inv_freq = rope->inv_freq;
+  a.positions = rope->positions; a.n_ctx = n_ctx; a.n_new = rope->n_new;
+  a.q_stride = rope->q_stride; a.k_stride = rope->k_stride; a.v_stride = rope->v_stride;
+  a.rot = rope->rot; a.interleaved = rope->interleaved;
+  a.eps = rope->eps; a.scale = rope->scale;
+  a.status = at<uint32_t>(workspace, 0);
+  if (dsa::launch_qk_norm_rope(sh, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+size_t dsa_window_workspace_size(const dsa_dims *dims) {
+  Shape sh;
+  if (make_shape(dims, &sh, true) != DSA_OK || sh.G > 128) return 0;
+  // the longest reach needs the most splits' room: no window is cut shorter than the prefix
+  return dsa::plan_window(sh, num_sms_current(), INT32_MAX, 0).total;
+}
+
+int dsa_window_launches(const dsa_dims *dims, const dsa_window *win) {
+  Shape sh;
+  const int rc = make_shape(dims, &sh, true);
+  if (rc != DSA_OK) return rc;
+  if (sh.G > 128) return DSA_ERR_UNSUPPORTED;
+  if (!good_window(win)) return DSA_ERR_INVALID_ARG;
+  return dsa::plan_window(sh, num_sms_current(), win->window, win->sinks).launches;
+}
+
+int dsa_window_attn(const void *q_blk, const void *k_cache, const void *v_cache,
+                    const void *blk_k, const void *blk_v, void *o_out, dsa_stream_t stream,
+                    const dsa_dims *dims, const dsa_window *win, const int32_t *n_ctx,
+                    void *workspace, size_t ws_bytes) {
+  Shape sh;
+  int rc = make_shape(dims, &sh, true);
+  if (rc != DSA_OK) return rc;
+  if (sh.G > 128) return DSA_ERR_UNSUPPORTED;
+  if (!good_window(win)) return DSA_ERR_INVALID_ARG;
+  if (!q_blk || !k_cache || !v_cache || !o_out || !n_ctx || !workspace || (blk_k == nullptr) != (blk_v == nullptr))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q_blk) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(blk_k) ||
+      !aligned16(blk_v) || !aligned16(o_out) || !aligned16(workspace))
+    return DSA_ERR_INVALID_ARG;
+  const dsa::PagedPlan plan = dsa::plan_window(sh, num_sms_current(), win->window, win->sinks);
+  if (ws_bytes < plan.total) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  dsa::PagedArgs a{};
+  a.q = bf(q_blk); a.k = bf(k_cache); a.v = bf(v_cache);
+  a.blk_k = bf(blk_k); a.blk_v = bf(blk_v);
+  a.n_ctx = n_ctx; a.n_new = win->n_new;
+  a.o_out = bf(o_out);
+  a.window = win->window; a.sinks = win->sinks; a.causal = win->causal;
+  a.status = at<uint32_t>(workspace, 0);
+  if (dsa::launch_window(sh, plan, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+int dsa_kv4_store(const void *blk_k, const void *blk_v, const dsa_kv4 *cache, dsa_stream_t stream,
+                  const dsa_dims *dims, const int32_t *n_ctx, const int32_t *n_new,
+                  void *workspace, size_t ws_bytes) {
+  Shape sh;
+  int rc = make_shape(dims, &sh, true);
+  if (rc != DSA_OK) return rc;
+  dsa::Kv4 c;
+  if (!blk_k || !blk_v || !n_ctx || !aligned16(blk_k) || !aligned16(blk_v) || !make_kv4(cache, &c))
+    return DSA_ERR_INVALID_ARG;
+  rc = check_header(workspace, ws_bytes);
+  if (rc != DSA_OK) return rc;
+  if (dsa::launch_kv4_store(sh, c, bf(blk_k), bf(blk_v), n_ctx, n_new, at<uint32_t>(workspace, 0),
+                            reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+int dsa_kv4_load(const dsa_kv4 *cache, void *k_out, void *v_out, dsa_stream_t stream,
+                 const dsa_dims *dims, const int32_t *start, const int32_t *n_new,
+                 void *workspace, size_t ws_bytes) {
+  Shape sh;
+  int rc = make_shape(dims, &sh, true);
+  if (rc != DSA_OK) return rc;
+  dsa::Kv4 c;
+  if (!k_out || !v_out || !start || !aligned16(k_out) || !aligned16(v_out) || !make_kv4(cache, &c))
+    return DSA_ERR_INVALID_ARG;
+  rc = check_header(workspace, ws_bytes);
+  if (rc != DSA_OK) return rc;
+  if (dsa::launch_kv4_load(sh, c, bf(k_out), bf(v_out), start, n_new, at<uint32_t>(workspace, 0),
+                           reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
+}
+
+size_t dsa_kv4_workspace_size(const dsa_dims *dims) {
+  Shape sh;
+  if (make_shape(dims, &sh) != DSA_OK || sh.G > 128) return 0;
+  const int n = num_sms_current();
+  return std::max(dsa::plan_kv4(sh, n, false).total, dsa::plan_kv4(sh, n, true).total);
+}
+
+int dsa_kv4_launches(const dsa_dims *dims, int32_t sparse) {
+  Shape sh;
+  const int rc = make_shape(dims, &sh);
+  if (rc != DSA_OK) return rc;
+  if (sh.G > 128) return DSA_ERR_UNSUPPORTED;
+  return dsa::plan_kv4(sh, num_sms_current(), sparse != 0).launches;
+}
+
+int dsa_kv4_attn(const void *q_blk, const dsa_kv4 *cache, const int32_t *idx, const void *blk_k,
+                 const void *blk_v, void *o_out, dsa_stream_t stream, const dsa_dims *dims,
+                 const int32_t *n_ctx, const int32_t *idx_cnt, const int32_t *n_new,
+                 void *workspace, size_t ws_bytes) {
+  Shape sh;
+  int rc = make_shape(dims, &sh);
+  if (rc != DSA_OK) return rc;
+  if (sh.G > 128) return DSA_ERR_UNSUPPORTED;
+  dsa::PagedArgs a{};
+  if (!q_blk || !o_out || !n_ctx || !workspace || (blk_k == nullptr) != (blk_v == nullptr) ||
+      (idx == nullptr) != (idx_cnt == nullptr) || !make_kv4(cache, &a.kv4))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q_blk) || !aligned16(blk_k) || !aligned16(blk_v) || !aligned16(o_out) || !aligned16(workspace))
+    return DSA_ERR_INVALID_ARG;
+  const dsa::PagedPlan plan = dsa::plan_kv4(sh, num_sms_current(), idx != nullptr);
+  if (ws_bytes < plan.total) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  a.q = bf(q_blk);
+  a.blk_k = bf(blk_k); a.blk_v = bf(blk_v);
+  a.idx = idx; a.idx_cnt = idx_cnt; a.n_ctx = n_ctx; a.n_new = n_new;
+  a.o_out = bf(o_out);
+  a.status = at<uint32_t>(workspace, 0);
+  if (dsa::launch_kv4_attn(sh, plan, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DSA_ERR_CUDA;
   return DSA_OK;
 }

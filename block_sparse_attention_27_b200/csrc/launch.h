@@ -133,4 +133,54 @@ int sparse_resident_cluster(const Shape &sh);
 cudaError_t launch_sparse(const Shape &sh, const SparsePlan &plan, const SparseArgs &a,
                           cudaStream_t stream);
 
+// ---- operators beside the passes ----
+// Token count of sequence s's block (n_new, else B) and page lookup are shared
+// by their kernels (paged.cuh).
+
+struct RopeArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *k_out, *v_out, *k_cache, *v_cache;
+  const __nv_bfloat16 *q_norm, *k_norm;
+  const float *inv_freq;
+  const int32_t *positions, *n_ctx, *n_new;
+  long long q_stride, k_stride, v_stride;
+  int rot, interleaved;
+  float eps, scale;
+  uint32_t *status;
+};
+constexpr int kRopeLaunches = 1;
+cudaError_t launch_qk_norm_rope(const Shape &sh, const RopeArgs &a, cudaStream_t stream);  // rope.cu
+
+// 4-bit cache: packed codes and scales of keys and values
+struct Kv4 {
+  uint8_t *k, *v;
+  __nv_bfloat16 *ks, *vs;
+};
+constexpr int kKv4StoreLaunches = 1;
+constexpr int kKv4LoadLaunches = 1;
+cudaError_t launch_kv4_store(const Shape &sh, const Kv4 &c, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
+                             const int32_t *n_ctx, const int32_t *n_new, uint32_t *status, cudaStream_t stream);
+cudaError_t launch_kv4_load(const Shape &sh, const Kv4 &c, __nv_bfloat16 *k, __nv_bfloat16 *v, const int32_t *start,
+                            const int32_t *n_new, uint32_t *status, cudaStream_t stream);
+
+// attention over a windowed bf16 cache or a 4-bit cache (paged_attn.cu)
+struct PagedArgs {
+  const __nv_bfloat16 *q, *k, *v;    // k, v: bf16 cache (windowed attention)
+  Kv4 kv4;                           // 4-bit cache
+  const __nv_bfloat16 *blk_k, *blk_v;
+  const int32_t *idx, *idx_cnt, *n_ctx, *n_new;
+  __nv_bfloat16 *o_out;
+  int window, sinks, causal;
+  uint32_t *status;
+};
+struct PagedPlan {
+  int splits;     // key splits per (sequence, KV head, row tile)
+  int launches;
+  size_t total;   // workspace bytes
+};
+PagedPlan plan_window(const Shape &sh, int num_sms, int window, int sinks);
+PagedPlan plan_kv4(const Shape &sh, int num_sms, bool sparse);
+cudaError_t launch_window(const Shape &sh, const PagedPlan &plan, const PagedArgs &a, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const Shape &sh, const PagedPlan &plan, const PagedArgs &a, cudaStream_t stream);
+
 }  // namespace dsa

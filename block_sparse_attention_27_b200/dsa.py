@@ -8,6 +8,7 @@ library is missing or no GPU is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -28,12 +29,18 @@ DSA_ERR_SCRATCH_LIMIT = -8
 # size of the library-held scratch array of dsa_select_static_scratch
 DSA_SELECT_STATIC_SCRATCH_BYTES = 16 << 20
 
+# smallest workspace of the operators that need only the status header
+WORKSPACE_HEADER_BYTES = 4096
+
 # every symbol include/dsa.h declares
 EXPORTED = ("dsa_select", "dsa_sparse_attn", "dsa_select_workspace_size",
             "dsa_sparse_workspace_size", "dsa_workspace_init", "dsa_get_status",
             "dsa_strerror", "dsa_kernels_per_call", "dsa_select_launches", "dsa_version",
             "dsa_select_static_scratch",
-            "dsa_merge_attn", "dsa_sparse_kernel")
+            "dsa_merge_attn", "dsa_sparse_kernel",
+            "dsa_qk_norm_rope", "dsa_window_attn", "dsa_window_workspace_size",
+            "dsa_window_launches", "dsa_kv4_store", "dsa_kv4_load", "dsa_kv4_attn",
+            "dsa_kv4_workspace_size", "dsa_kv4_launches")
 
 
 class DsaError(RuntimeError):
@@ -51,6 +58,25 @@ class dsa_dims(ctypes.Structure):
                 ("head_budget", ctypes.c_int32), ("active", ctypes.c_void_p),
                 ("prefix_o_cache", ctypes.c_void_p), ("prefix_lse_cache", ctypes.c_void_p),
                 ("early_gather", ctypes.c_int32)]
+
+
+class dsa_rope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("inv_freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class dsa_window(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("n_new", ctypes.c_void_p)]
+
+
+class dsa_kv4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -100,6 +126,26 @@ def open_library(path: str):
     lib.dsa_kernels_per_call.argtypes = [ci]
     lib.dsa_select_launches.restype = ci
     lib.dsa_select_launches.argtypes = [dims_p]
+    rope_p, win_p = ctypes.POINTER(dsa_rope), ctypes.POINTER(dsa_window)
+    kv4_p = ctypes.POINTER(dsa_kv4)
+    lib.dsa_qk_norm_rope.restype = ci
+    lib.dsa_qk_norm_rope.argtypes = [vp] * 9 + [dims_p, rope_p, vp, vp, sz]
+    lib.dsa_window_attn.restype = ci
+    lib.dsa_window_attn.argtypes = [vp] * 7 + [dims_p, win_p, vp, vp, sz]
+    lib.dsa_window_workspace_size.restype = sz
+    lib.dsa_window_workspace_size.argtypes = [dims_p]
+    lib.dsa_window_launches.restype = ci
+    lib.dsa_window_launches.argtypes = [dims_p, win_p]
+    lib.dsa_kv4_store.restype = ci
+    lib.dsa_kv4_store.argtypes = [vp, vp, kv4_p, vp, dims_p, vp, vp, vp, sz]
+    lib.dsa_kv4_load.restype = ci
+    lib.dsa_kv4_load.argtypes = [kv4_p, vp, vp, vp, dims_p, vp, vp, vp, sz]
+    lib.dsa_kv4_attn.restype = ci
+    lib.dsa_kv4_attn.argtypes = [vp, kv4_p, vp, vp, vp, vp, vp, dims_p, vp, vp, vp, vp, sz]
+    lib.dsa_kv4_workspace_size.restype = sz
+    lib.dsa_kv4_workspace_size.argtypes = [dims_p]
+    lib.dsa_kv4_launches.restype = ci
+    lib.dsa_kv4_launches.argtypes = [dims_p, ctypes.c_int32]
     lib.dsa_sparse_kernel.restype = ci
     lib.dsa_sparse_kernel.argtypes = [dims_p]
     return lib
@@ -107,7 +153,7 @@ def open_library(path: str):
 
 def kernels_per_call(pass_: int) -> int:
     """Kernel launches per call: 0 = dsa_select (groups in one launch), 1 = dsa_sparse_attn,
-    2 = dsa_merge_attn."""
+    2 = dsa_merge_attn, 3 = dsa_qk_norm_rope, 4 = dsa_kv4_store, 5 = dsa_kv4_load."""
     return int(load().dsa_kernels_per_call(int(pass_)))
 
 
@@ -297,6 +343,265 @@ def dsa_merge_attn(o_a, lse_a, o_b, lse_b, o_out, lse_out=None, stream=None):
                                _ptr(lse_out), rows, d, _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, "dsa_merge_attn")
+
+
+# ------------------------------------------- operators beside the two passes ----
+def _arg(t, name, dtype, shape=None):
+    """Address of a contiguous CUDA tensor on the current device, checked; None stays None
+    only where the caller allows it (it does not call this then)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape=None):
+    return None if t is None else _arg(t, name, dtype, shape)
+
+
+def _ws(workspace):
+    return _arg(workspace.buf, "workspace", torch.uint8)
+
+
+def _raw_stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _call(rc, what):
+    if rc != DSA_OK:
+        raise DsaError(rc, what)
+
+
+def rope_inv_freq(rot, base=10000.0, *, scaling=None, device="cuda"):
+    """(inv_freq fp32 [rot/2], scale) of dsa_qk_norm_rope: radians per position of each pair,
+    base ** (-2i / rot), computed in fp64, and the factor on cos and sin.
+
+    scaling, for contexts longer than the trained one:
+      None
+      ("linear", f)      every position divided by f
+      ("ntk", f)         the base raised so that the slowest pair is stretched f times
+      ("yarn", f, n0)    pairs that turn more than 32 times within the trained length n0 are
+                         kept, those that turn less than once are stretched f times, a linear
+                         ramp over the pair index between; cos and sin times 0.1 ln f + 1
+    """
+    if rot < 8 or rot % 8:
+        raise ValueError("rot must be a positive multiple of 8")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    freq, scale = float(base) ** (-2 * i / rot), 1.0
+    if scaling is not None:
+        kind, f = scaling[0], float(scaling[1])
+        if f < 1:
+            raise ValueError("the scaling factor must be at least 1")
+        if kind == "linear":
+            freq = freq / f
+        elif kind == "ntk":
+            freq = (float(base) * f ** (rot / (rot - 2))) ** (-2 * i / rot)
+        elif kind == "yarn":
+            n0 = float(scaling[2])
+
+            def pair(turns):  # index of the pair that turns that often within n0 positions
+                return rot * math.log(n0 / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+            lo = max(0.0, float(math.floor(pair(32.0))))
+            hi = min(rot / 2 - 1.0, float(math.ceil(pair(1.0))))
+            ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            freq = freq * (1 - ramp) + freq / f * ramp
+            scale = 0.1 * math.log(f) + 1.0
+        else:
+            raise ValueError(f"unknown scaling {kind!r}")
+    return freq.to(torch.float32).to(device), scale
+
+
+class Rope:
+    """What dsa_qk_norm_rope needs of a layer: frequencies, layout and norm weights
+    (include/dsa.h, dsa_rope).  Keeps the tensors alive."""
+
+    def __init__(self, inv_freq, rot, *, interleaved=False, scale=1.0, eps=1e-6, q_norm=None,
+                 k_norm=None):
+        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
+        self.rot, self.scale, self.eps = int(rot), float(scale), float(eps)
+        self.interleaved = int(bool(interleaved))
+        _arg(inv_freq, "inv_freq", torch.float32, (self.rot // 2,))
+        for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if w is not None:
+                _arg(w, name, torch.bfloat16)
+                if w.dim() != 1:
+                    raise ValueError(f"{name} must have one dimension")
+
+
+def _projection(t, name, dims, H):
+    """Address and token stride of a projection [S, B, H, d] whose tokens may be a view into a
+    packed row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (dims.S, dims.B, H, dims.d):
+        raise ValueError(f"{name} must have shape {(dims.S, dims.B, H, dims.d)}, got {tuple(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    st = t.stride()
+    token = st[1] if dims.B > 1 else st[0] if dims.S > 1 else H * dims.d
+    if (dims.d > 1 and st[3] != 1) or (H > 1 and st[2] != dims.d) or (dims.S > 1 and st[0] != dims.B * token):
+        raise ValueError(f"{name}: a token's heads must be contiguous and the tokens evenly spaced")
+    return t.data_ptr(), token
+
+
+def dsa_qk_norm_rope(q, k, v, q_out, k_out=None, v_out=None, stream=None, *, dims: dsa_dims,
+                     rope: Rope, n_ctx=None, workspace: Workspace, positions=None, n_new=None,
+                     k_cache=None, v_cache=None):
+    """Norm of each head's query and key, rotation by position, and append to the paged cache in
+    one pass (see include/dsa.h).  q, k, v: bf16 [S, B, H, d], possibly views into a packed
+    projection; k and v go to k_out / v_out (contiguous) and / or the cache."""
+    S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
+    bf = torch.bfloat16
+    r = dsa_rope(rope.rot, rope.interleaved, rope.eps, rope.scale, rope.inv_freq.data_ptr())
+    for w in (rope.q_norm, rope.k_norm):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"norm weights must have {d} elements")
+    r.q_norm = None if rope.q_norm is None else rope.q_norm.data_ptr()
+    r.k_norm = None if rope.k_norm is None else rope.k_norm.data_ptr()
+    r.positions = _opt(positions, "positions", torch.int32, (S, B))
+    r.n_new = _opt(n_new, "n_new", torch.int32, (S,))
+    pq = pk = pv = None
+    if q is not None:
+        pq, r.q_stride = _projection(q, "q", dims, Hq)
+    if k is not None:
+        pk, r.k_stride = _projection(k, "k", dims, Hkv)
+    if v is not None:
+        pv, r.v_stride = _projection(v, "v", dims, Hkv)
+    cache = (dims.n_phys, Hkv, dims.page, d)
+    _call(load().dsa_qk_norm_rope(
+        pq, pk, pv, _opt(q_out, "q_out", bf, (S, B, Hq, d)), _opt(k_out, "k_out", bf, (S, B, Hkv, d)),
+        _opt(v_out, "v_out", bf, (S, B, Hkv, d)), _opt(k_cache, "k_cache", bf, cache),
+        _opt(v_cache, "v_cache", bf, cache), _raw_stream(stream), ctypes.byref(dims), ctypes.byref(r),
+        _opt(n_ctx, "n_ctx", torch.int32, (S,)), _ws(workspace), workspace.nbytes), "dsa_qk_norm_rope")
+
+
+def window_workspace_size(dims: dsa_dims) -> int:
+    return int(load().dsa_window_workspace_size(ctypes.byref(dims)))
+
+
+def window_launches(dims: dsa_dims, window, sinks=0, causal=False) -> int:
+    rc = int(load().dsa_window_launches(ctypes.byref(dims), ctypes.byref(dsa_window(window, sinks, int(causal), None))))
+    if rc < 0:
+        raise DsaError(rc, "dsa_window_launches")
+    return rc
+
+
+def dsa_window_attn(q_blk, k_cache, v_cache, blk_k, blk_v, o_out, stream=None, *, dims: dsa_dims,
+                    window, sinks=0, causal=False, n_ctx, workspace: Workspace, n_new=None,
+                    lse_out=None):
+    """Attention with a sliding window and `sinks` first tokens that stay visible (see
+    include/dsa.h).  blk_k = blk_v = None: the prefix alone."""
+    S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
+    bf = torch.bfloat16
+    cache, blk = (dims.n_phys, Hkv, dims.page, d), (S, B, Hkv, d)
+    w = dsa_window(int(window), int(sinks), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,)))
+    dims = _with_lse_out(dims, lse_out)
+    _call(load().dsa_window_attn(
+        _arg(q_blk, "q_blk", bf, (S, B, Hq, d)), _arg(k_cache, "k_cache", bf, cache),
+        _arg(v_cache, "v_cache", bf, cache), _opt(blk_k, "blk_k", bf, blk), _opt(blk_v, "blk_v", bf, blk),
+        _arg(o_out, "o_out", bf, (S, B, Hq, d)), _raw_stream(stream), ctypes.byref(dims), ctypes.byref(w),
+        _arg(n_ctx, "n_ctx", torch.int32, (S,)), _ws(workspace), workspace.nbytes), "dsa_window_attn")
+
+
+def _with_lse_out(dims: dsa_dims, lse_out) -> dsa_dims:
+    """dims for one call with its log-sum-exp output: that of the argument, else none."""
+    if lse_out is None and not dims.lse_out:
+        return dims
+    d = dsa_dims.from_buffer_copy(dims)
+    if lse_out is not None:
+        d.lse_out = _arg(lse_out, "lse_out", torch.float32, (dims.S, dims.B, dims.Hq))
+    return d
+
+
+class Kv4Cache:
+    """A paged cache in 4 bits (include/dsa.h, dsa_kv4): k, v uint8 [n_phys, Hkv, page, d/2],
+    k_scale, v_scale bf16 [n_phys, Hkv, page, d/32]."""
+
+    GROUP = 32
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must have 4 dimensions")
+        n_phys, Hkv, page, half = k.shape
+        codes, scales = tuple(k.shape), (n_phys, Hkv, page, 2 * half // self.GROUP)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.shape = (n_phys, Hkv, page, 2 * half)
+        self.c = dsa_kv4(_arg(k, "k", torch.uint8, codes), _arg(v, "v", torch.uint8, codes),
+                         _arg(k_scale, "k_scale", torch.bfloat16, scales),
+                         _arg(v_scale, "v_scale", torch.bfloat16, scales))
+
+    @classmethod
+    def zeros(cls, n_phys, Hkv, page, d, device=None):
+        dev = device or "cuda"
+        codes = [torch.zeros((n_phys, Hkv, page, d // 2), dtype=torch.uint8, device=dev) for _ in range(2)]
+        scales = [torch.zeros((n_phys, Hkv, page, d // cls.GROUP), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        return cls(*codes, *scales)
+
+    def _fits(self, dims):
+        if self.shape != (dims.n_phys, dims.Hkv, dims.page, dims.d):
+            raise ValueError(f"the 4-bit cache holds {self.shape}, dims say "
+                             f"{(dims.n_phys, dims.Hkv, dims.page, dims.d)}")
+        if self.k.device.index != torch.cuda.current_device():
+            raise ValueError(f"the 4-bit cache is on {self.k.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return ctypes.byref(self.c)
+
+
+def dsa_kv4_store(blk_k, blk_v, cache: Kv4Cache, stream=None, *, dims: dsa_dims, n_ctx,
+                  workspace: Workspace, n_new=None):
+    """Appends the block's keys and values to the 4-bit cache at n_ctx[s] + b (see include/dsa.h)."""
+    bf, blk = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d)
+    _call(load().dsa_kv4_store(
+        _arg(blk_k, "blk_k", bf, blk), _arg(blk_v, "blk_v", bf, blk), cache._fits(dims), _raw_stream(stream),
+        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (dims.S,)),
+        _opt(n_new, "n_new", torch.int32, (dims.S,)), _ws(workspace), workspace.nbytes), "dsa_kv4_store")
+
+
+def dsa_kv4_load(cache: Kv4Cache, k_out, v_out, stream=None, *, dims: dsa_dims, start,
+                 workspace: Workspace, n_new=None):
+    """Reads tokens start[s] + b of the 4-bit cache back in bf16 (see include/dsa.h)."""
+    bf, blk = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d)
+    _call(load().dsa_kv4_load(
+        cache._fits(dims), _arg(k_out, "k_out", bf, blk), _arg(v_out, "v_out", bf, blk), _raw_stream(stream),
+        ctypes.byref(dims), _arg(start, "start", torch.int32, (dims.S,)),
+        _opt(n_new, "n_new", torch.int32, (dims.S,)), _ws(workspace), workspace.nbytes), "dsa_kv4_load")
+
+
+def kv4_workspace_size(dims: dsa_dims) -> int:
+    return int(load().dsa_kv4_workspace_size(ctypes.byref(dims)))
+
+
+def kv4_launches(dims: dsa_dims, sparse: bool) -> int:
+    rc = int(load().dsa_kv4_launches(ctypes.byref(dims), int(bool(sparse))))
+    if rc < 0:
+        raise DsaError(rc, "dsa_kv4_launches")
+    return rc
+
+
+def dsa_kv4_attn(q_blk, cache: Kv4Cache, idx, blk_k, blk_v, o_out, stream=None, *, dims: dsa_dims,
+                 n_ctx, workspace: Workspace, idx_cnt=None, n_new=None, lse_out=None):
+    """The sparse pass over a 4-bit cache: the pages idx names, or every page where idx is None,
+    and the block's own tokens (see include/dsa.h)."""
+    S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
+    bf, blk = torch.bfloat16, (S, B, Hkv, d)
+    dims = _with_lse_out(dims, lse_out)
+    _call(load().dsa_kv4_attn(
+        _arg(q_blk, "q_blk", bf, (S, B, Hq, d)), cache._fits(dims),
+        _opt(idx, "idx", torch.int32, (S, Hkv, dims.kmax)), _opt(blk_k, "blk_k", bf, blk),
+        _opt(blk_v, "blk_v", bf, blk), _arg(o_out, "o_out", bf, (S, B, Hq, d)), _raw_stream(stream),
+        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (S,)),
+        _opt(idx_cnt, "idx_cnt", torch.int32, (S, Hkv)), _opt(n_new, "n_new", torch.int32, (S,)),
+        _ws(workspace), workspace.nbytes), "dsa_kv4_attn")
 
 
 class DeviceWorkload:

@@ -280,12 +280,149 @@ int dsa_select_static_scratch(const void *q_blk, const void *k_cache, const void
 int dsa_merge_attn(const void *o_a, const float *lse_a, const void *o_b, const float *lse_b,
                    void *o_out, float *lse_out, int64_t rows, int32_t d, dsa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators beside the two passes: the step from a layer's projections to the
+ * queries and keys the passes take (dsa_qk_norm_rope, which also appends to the
+ * paged cache), attention of layers with a sliding window (dsa_window_attn), and
+ * a cache held in 4 bits (dsa_kv4_store, dsa_kv4_load, dsa_kv4_attn).
+ *
+ * They take the layouts, dims, workspace and status rules above.  Of dsa_dims they
+ * use S, B, Hq, Hkv, d, page, max_pages, n_phys, page_table, and where stated kmax
+ * and lse_out.  Unless stated otherwise B is not bounded by B * Hq/Hkv <= 256, so a
+ * whole prompt is one call; S * B * (Hq + 2 Hkv) < 2^31.
+ *
+ *  n_new [S]   (device int32, or NULL = B for every sequence): tokens of each
+ *              sequence's block that exist, so that a batch of blocks of different
+ *              lengths is one padded call.  Rows b >= n_new[s] are neither read nor
+ *              written and are no keys.  A value outside [0, B] is clamped and
+ *              reported as DSA_ERR_BAD_INDEX.
+ *
+ * A token of the block sits at position n_ctx[s] + b.  A call that writes the cache
+ * skips a token whose page is not below max_pages, or whose page-table entry is
+ * outside the cache, and reports DSA_ERR_BAD_INDEX.  A kernel that writes the cache
+ * right before a dsa_sparse_attn call excludes dims->early_gather for that call
+ * (see there).
+ * ------------------------------------------------------------------------ */
+
+/* Smallest workspace of the operators that need only the status header. */
+#define DSA_WORKSPACE_HEADER_BYTES ((size_t)4096)
+
+typedef struct dsa_rope {
+  int32_t rot;              /* leading elements of a head that are rotated: a multiple of 8, 8 <= rot <= d */
+  int32_t interleaved;      /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1), i < rot/2 */
+  float eps;                /* of the norms, > 0 */
+  float scale;              /* factor on cos and sin (1 without long-context scaling), finite */
+  const float *inv_freq;    /* device fp32 [rot/2]: radians per position of each pair, any
+                               long-context scaling already in it */
+  const int32_t *positions; /* device int32 [S, B], or NULL = n_ctx[s] + b */
+  const void *q_norm;       /* device bf16 [d], 16-byte aligned: weight of the queries' norm; NULL = no norm */
+  const void *k_norm;       /* the same for the keys */
+  const int32_t *n_new;     /* device int32 [S] or NULL, see above */
+  int64_t q_stride;         /* elements between consecutive tokens of q, k and v: multiples of 8, at */
+  int64_t k_stride;         /*   least H * d, so that a packed projection is read in place */
+  int64_t v_stride;
+} dsa_rope;
+
+/*
+ * Norm of each head's query and key and rotation by position, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * w        (x itself where w is NULL)
+ *   pair (a, b) of y -> (a cos - b sin, b cos + a sin) * scale,
+ *   angle = position * inv_freq[i],
+ * elements from rot on stay y; computed in fp32, the angle in fp64, rounded once to
+ * bf16.  v is copied.  q, k, v: bf16 [S, B, H, d] with H * d contiguous elements per
+ * token and dsa_rope's strides between tokens.  q_out [S, B, Hq, d] contiguous;
+ * k_out, v_out [S, B, Hkv, d] contiguous (the passes' blk_k, blk_v) and / or
+ * k_cache, v_cache: the token's row at its page and slot (append).  Each of q, k, v
+ * is optional and NULL together with its outputs; an output may be its own input
+ * (same address and stride), other overlaps are not allowed.  n_ctx may be NULL when
+ * positions are given and no cache is written.  One kernel launch.
+ */
+int dsa_qk_norm_rope(const void *q, const void *k, const void *v, void *q_out, void *k_out,
+                     void *v_out, void *k_cache, void *v_cache, dsa_stream_t stream,
+                     const dsa_dims *dims, const dsa_rope *rope, const int32_t *n_ctx,
+                     void *workspace, size_t ws_bytes);
+
+typedef struct dsa_window {
+  int32_t window;        /* >= 1: keys less than `window` positions away are visible */
+  int32_t sinks;         /* >= 0: the first `sinks` tokens stay visible */
+  int32_t causal;        /* 1: no key after the query's position is visible */
+  const int32_t *n_new;  /* device int32 [S] or NULL, see above */
+} dsa_window;
+
+/*
+ * Attention with a sliding window and first tokens that stay visible.  The query of
+ * token b sits at p = n_ctx[s] + b.  Keys are the prefix (positions j < n_ctx[s], from
+ * the cache) and the block's own tokens (position n_ctx[s] + u, from blk_k / blk_v;
+ * both NULL: the prefix alone).  A key at j takes part when
+ *   (j < sinks or |p - j| < window) and (not causal or j <= p).
+ * Softmax with scale 1/sqrt(d); o_out [S, B, Hq, d]; dims->lse_out as above.  A row
+ * without a visible key gets o = 0 and lse = -inf.  Pages that hold no visible token
+ * are not read and their page-table entries not looked at, so they may be freed.
+ * Values of tokens that no query of a row tile (128 / (Hq/Hkv) tokens) sees never reach the
+ * output; a non-finite value that one query of the tile sees may reach the tile's others.
+ * Hq/Hkv <= 128.  dsa_window_launches() kernel launches.
+ */
+int dsa_window_attn(const void *q_blk, const void *k_cache, const void *v_cache,
+                    const void *blk_k, const void *blk_v, void *o_out, dsa_stream_t stream,
+                    const dsa_dims *dims, const dsa_window *win, const int32_t *n_ctx,
+                    void *workspace, size_t ws_bytes);
+
+/* Workspace bytes (for any window, sinks and causal) and kernel launches of a call with
+ * these dims on the current device (0 and a negative code if dims is invalid). */
+size_t dsa_window_workspace_size(const dsa_dims *dims);
+int dsa_window_launches(const dsa_dims *dims, const dsa_window *win);
+
+/*
+ * A paged cache in 4 bits.  A row of d values is d/32 groups.  Group: scale s = the
+ * smallest number with five significant bits that is >= max|x| / 7, held in bf16 (0 where
+ * max|x| < 2^-100; NaN where a value is not finite or >= 2^120 in magnitude); code =
+ * x / s rounded to the nearest integer (ties to even), plus 8; the value held is
+ * (code - 8) * s, which bf16 represents exactly.  Eight consecutive values are one
+ * little-endian 32-bit word: value 2i in bits 4i..4i+3, value 2i + 1 in bits
+ * 16+4i..19+4i, i = 0..3.
+ */
+typedef struct dsa_kv4 {
+  void *k;        /* device uint8 [n_phys, Hkv, page, d/2], 16-byte aligned like the others */
+  void *v;
+  void *k_scale;  /* device bf16 [n_phys, Hkv, page, d/32] */
+  void *v_scale;
+} dsa_kv4;
+
+/* Appends the block's keys and values (bf16 [S, B, Hkv, d]) to the 4-bit cache at
+ * positions n_ctx[s] + b.  Every other byte of the cache is left as it was.  One launch. */
+int dsa_kv4_store(const void *blk_k, const void *blk_v, const dsa_kv4 *cache, dsa_stream_t stream,
+                  const dsa_dims *dims, const int32_t *n_ctx, const int32_t *n_new,
+                  void *workspace, size_t ws_bytes);
+
+/* Reads tokens start[s] + b, b < n_new[s], back: k_out, v_out bf16 [S, B, Hkv, d].  A token
+ * outside the table or the cache is skipped (DSA_ERR_BAD_INDEX).  One launch. */
+int dsa_kv4_load(const dsa_kv4 *cache, void *k_out, void *v_out, dsa_stream_t stream,
+                 const dsa_dims *dims, const int32_t *start, const int32_t *n_new,
+                 void *workspace, size_t ws_bytes);
+
+/*
+ * The sparse pass over a 4-bit cache: each query row attends to the prefix tokens of
+ * the pages idx[s, h, 0 .. idx_cnt-1] (rules of dsa_sparse_attn), or of every page where
+ * idx and idx_cnt are NULL, and to the block's own n_new[s] tokens (bf16, no mask inside the
+ * block; blk_k and blk_v both NULL: the prefix alone).  o_out and dims->lse_out as above; a
+ * row without a key gets o = 0, lse = -inf.  B * Hq/Hkv <= 256.  dsa_kv4_launches() launches.
+ */
+int dsa_kv4_attn(const void *q_blk, const dsa_kv4 *cache, const int32_t *idx, const void *blk_k,
+                 const void *blk_v, void *o_out, dsa_stream_t stream, const dsa_dims *dims,
+                 const int32_t *n_ctx, const int32_t *idx_cnt, const int32_t *n_new,
+                 void *workspace, size_t ws_bytes);
+
+/* Workspace bytes (with or without idx) and kernel launches; `sparse` = idx is given. */
+size_t dsa_kv4_workspace_size(const dsa_dims *dims);
+int dsa_kv4_launches(const dsa_dims *dims, int32_t sparse);
+
 /* Static description of a status code. */
 const char *dsa_strerror(int code);
 
 /* Number of kernel launches one call issues on its stream: pass 0 = dsa_select
  * when its groups fit in one launch (dsa_select_launches() gives the count for
- * a shape), pass 1 = dsa_sparse_attn, pass 2 = dsa_merge_attn
+ * a shape), pass 1 = dsa_sparse_attn, pass 2 = dsa_merge_attn, pass 3 =
+ * dsa_qk_norm_rope, pass 4 = dsa_kv4_store, pass 5 = dsa_kv4_load
  * (DSA_ERR_INVALID_ARG otherwise).  Useful when capturing calls into a CUDA
  * graph or counting launches. */
 int dsa_kernels_per_call(int pass);
