@@ -425,19 +425,34 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // row maximum
+        // The row's scores, all 128 in registers; with the 4-bit cache's warps beside it a
+        // thread has 128 registers: it holds the first 64, and reads the others twice.
+        constexpr int kHold = KV4 ? 64 : 128;
+        uint32_t x[kHold];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (KV4) {
+          tmem_ld64(sc, x);
+        } else {
+          tmem_ld64x2(sc, *reinterpret_cast<uint32_t(*)[64]>(&x[0]), sc + 64, *reinterpret_cast<uint32_t(*)[64]>(&x[64]));
+        }
+        auto hide = [&](uint32_t *y, int w) {  // scores of 32 keys that take no part: -inf
+          if (bits[w] == ~0u) return;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t x[32];
-          tmem_ld32(sc + 32 * w, x);
-          if (bits[w] == ~0u) {
+          for (int j = 0; j < 32; ++j)
+            if (!((bits[w] >> j) & 1u)) y[j] = 0xff800000u;
+        };
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
-          } else {
+        for (int w = 0; w < kHold / 32; ++w) hide(x + 32 * w, w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if ((bits[w] >> j) & 1u) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+        for (int j = 0; j < kHold; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+        if constexpr (KV4) {
+#pragma unroll
+          for (int w = 2; w < 4; ++w) {
+            uint32_t y[32];
+            tmem_ld32(sc + 32 * w, y);
+            hide(y, w);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(y[j]));
           }
         }
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2;
@@ -461,26 +476,31 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           }
         }
         const float mu = m_used == -INFINITY ? 0.f : m_used;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t x[32], pk[16];
-          tmem_ld32(sc + 32 * w, x);
-          if (bits[w] != ~0u) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((bits[w] >> j) & 1u)) x[j] = 0xff800000u;  // -inf
-          }
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 scale2 = make_float2(sh.sl2, sh.sl2), mu2 = make_float2(-mu, -mu);
+        auto emit = [&](const uint32_t *y, int w) {  // 32 probabilities, over S columns already read
+          uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(x[2 * j]), sh.sl2, -mu));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(x[2 * j + 1]), sh.sl2, -mu));
-            sum[j & 3] += p0 + p1;
-            pk[j] = pack_bf16x2(p0, p1);
+            const float2 e = fma2(make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), scale2, mu2);
+            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            sum[j & 1] = add2(sum[j & 1], p);
+            pk[j] = pack_bf16x2(p.x, p.y);
           }
-          tmem_st16(sc + 16 * w, pk);  // over S columns already read
+          tmem_st16_async(sc + 16 * w, pk);
+        };
+#pragma unroll
+        for (int w = 0; w < kHold / 32; ++w) emit(x + 32 * w, w);
+        if constexpr (KV4) {
+          tmem_ld64(sc + 64, x);
+#pragma unroll
+          for (int w = 2; w < 4; ++w) {
+            hide(x + 32 * (w - 2), w);
+            emit(x + 32 * (w - 2), w);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc_fence_before();
         mbar_arrive(p_full(g));
       }
