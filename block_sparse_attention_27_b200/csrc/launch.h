@@ -174,7 +174,8 @@ struct PagedArgs {
   uint32_t *status;
 };
 struct PagedPlan {
-  int splits;     // key splits per (sequence, KV head, row tile)
+  int ctas;
+  int shared_out; // 1: the units' tiles are cut into equal shares, 0: CTAs take whole units
   int launches;
   size_t total;   // workspace bytes
 };

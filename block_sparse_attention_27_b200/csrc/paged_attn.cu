@@ -5,19 +5,29 @@
 //   x_j = q.k_j / sqrt(d) over the visible keys j,  o = sum_j e^(x_j - m) v_j / l,
 //   l = sum_j e^(x_j - m),  lse = m + ln l
 //
-// One CTA takes up to 128 query rows (token, head of one KV head's group) and a share
-// of their keys in tiles of 128: pages that hold a visible token, then block tokens.
-// Rows whose keys are shared out over several CTAs leave (O, m, l) in fp32 in the
-// workspace, and paged_merge joins them.
+// A unit is up to 128 query rows (token, head of one KV head's group) and their keys in
+// tiles of 128: pages that hold a visible token, then block tokens.  The grid is one CTA
+// per SM, and each CTA walks through units without stopping between them.  With few
+// units, all units' tiles in a row are cut into equal shares, so that sequences of any
+// lengths load the SMs alike; a unit that a share's border cuts leaves (O, m, l) of each
+// piece in fp32 in the workspace, and paged_merge joins the pieces in order.  With many
+// units (kManyUnits per CTA) each CTA takes whole ones.
 //
-// Warp roles: warp 0 loads the queries and (bf16 cache) the key tiles with TMA; warp 1
-// owns TMEM and issues the MMAs; warps 2..9 are two softmax groups that take alternate
-// tiles, a thread per row; warps 10..13 (4-bit cache) turn packed rows into bf16 tiles.
-//   S = Q K^T (128 x 128, TMEM), P = 2^(S - m) in bf16 over S's first 64 columns,
-//   O += P V (TMEM, one accumulator per group), joined at the end.
-// The reference maximum of a row moves only when a tile beats it by 2^8, so O is
-// rarely rescaled.  Sums and outputs are held in fp32, P alone in bf16 (the type of V,
-// which one MMA takes both operands in).
+// Warps:
+//   0        K tiles (TMA boxes, or 16-byte asynchronous copies for pages under 64
+//            tokens: a box costs the TMA unit about 90 ns whatever its size, and 32 boxes
+//            of 2 KB per tile held decoding at 3.1 TB/s), the tiles' positions
+//   1        TMEM; the MMAs
+//   2..9     two softmax groups of 128 threads, a thread per row, alternate tiles
+//   10, 11   V tiles; the queries
+//   4-bit cache: 0 the queries, 10..11 and 12..13 unpack K and V rows into bf16 tiles
+//
+//   S = Q K^T (128 x 128) into one of three TMEM buffers, P = 2^(S - m) in bf16 over its
+//   first 64 columns, O += P V (TMEM).  S runs two tiles ahead of P.
+// A row's reference maximum m is common to the groups (shared memory): the group of tile
+// k takes it from the group of tile k - 1 and moves it only when its tile beats it by
+// 2^8, so O is rarely rescaled.  Sums, maxima and outputs are held in fp32, P alone in
+// bf16: one MMA takes both operands in one type, and V is bf16.
 #include <climits>
 
 #include "paged.cuh"
@@ -31,25 +41,42 @@ constexpr int kBN = 128;  // keys of a tile
 constexpr int kRowsPerTile = 128;
 constexpr int kNever = INT_MAX;  // position of a key that takes no part
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kTabs = 8;        // tiles whose positions are kept: six are in flight at most
+constexpr int kMinTiles = 2;    // least tiles of a share
+constexpr int kManyUnits = 8;   // units per CTA from which shares are whole units
+constexpr int kUnitsPerThread = 4;  // of the scan over the units' tiles: 8 * 148 <= 4 * 320
 
 template <int D, bool KV4>
 struct Cfg {
   static constexpr int kHalves = D / 64;
-  static constexpr int kStages = D == 128 ? 3 : 5;
-  static constexpr int kThreads = KV4 ? 448 : 320;
+  static constexpr int kStages = KV4 ? 2 : D == 128 ? 3 : 5;
+  static constexpr int kThreads = KV4 ? 448 : 384;
   static constexpr uint32_t kHalf = 128u * 128u;           // 128 rows x 128 B
   static constexpr uint32_t kTile = kHalves * kHalf;       // one K or V tile, or Q
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kTile;
   static constexpr uint32_t kOffV = kOffK + kStages * kTile;
-  static constexpr uint32_t kOffBar = kOffV + kStages * kTile;
-  static constexpr int kNumBars = 4 * kStages + 8;
-  static constexpr uint32_t kOffTab = kOffBar + kNumBars * 8;      // per stage: 8 positions, flags, end
-  static constexpr uint32_t kOffMisc = kOffTab + kStages * 48;     // TMEM address, abort flag
-  static constexpr uint32_t kAlloc = kOffMisc + 16 + 1024;         // room to align the base to 1 KB
-  static constexpr uint32_t kOffML = kOffQ;                        // [2][128] (m, l) once Q is dead
-  static constexpr uint32_t kTmemO = 2 * kBN;
+  // 4-bit cache: packed tiles on their way in, three each for K and V: codes, then scales
+  static constexpr int kRawSlots = 3;
+  static constexpr uint32_t kRawCodes = kBN * D / 2;
+  static constexpr uint32_t kRaw = kRawCodes + kBN * (D / kKv4Group) * 2;
+  static constexpr uint32_t kOffRaw = kOffV + kStages * kTile;
+  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? 2 * kRawSlots * kRaw : 0);
+  static constexpr int kNumBars = 4 * kStages + kTabs + 18;
+  static constexpr uint32_t kOffTab = kOffBar + kNumBars * 8;      // per tile: 8 positions, flags, end
+  static constexpr uint32_t kOffMisc = kOffTab + kTabs * 40;       // TMEM address, abort flag, scan result
+  static constexpr uint32_t kOffM = kOffMisc + 32;                 // [128] reference maxima
+  static constexpr uint32_t kOffL = kOffM + 512;                   // [128] sums on their way between groups
+  static constexpr uint32_t kAlloc = kOffL + 512 + 1024;           // room to align the base to 1 KB
+  static constexpr uint32_t kTmemO = 3 * kBN;
   static constexpr uint32_t kTmemCols = 512;
+  static_assert(kAlloc <= 232448, "shared memory of a CTA");
+};
+
+// A piece of a unit in the workspace: which, and whether it holds the unit's first or
+// last tile.
+struct Piece {
+  int unit, begins, ends, pad;
 };
 
 struct Params {
@@ -57,19 +84,22 @@ struct Params {
   PagedArgs a;
   int bpt;        // block tokens of a row tile
   int rowtiles;
-  int splits;
+  int units;
+  int shared_out; // 1: equal shares of all tiles, 0: whole units
   int box_blk;    // block tokens of one TMA box
-  float *part_o;  // [unit][split][rows][D]
+  Piece *piece;   // [CTA][2]: the unit that the CTA's share enters in its middle, the one it leaves
+  float *part_o;  // [CTA][2][rows][D]
   float2 *part_ml;
 };
 
-// What a CTA attends to: a list of pages and two ranges of block tokens.
+// What a unit attends to: a list of pages and two ranges of block tokens.
 struct Keys {
-  int n, nb;          // prefix and block tokens
-  int nsp, wp0, npg;  // pages: sinks' pages 0..nsp-1, then wp0.. ; npg in all (or idx entries)
-  int pt;             // tiles of pages
-  int ua, ub0, ub;    // block tokens [0, ua) and [ub0, ub)
-  int ta, tiles;      // tiles of the first range; tiles in all
+  int s, h, b0, rows;  // sequence, KV head, first token, query rows
+  int n, nb;           // prefix and block tokens
+  int nsp, wp0, npg;   // pages: sinks' pages 0..nsp-1, then wp0.. ; npg in all (or idx entries)
+  int pt;              // tiles of pages
+  int ua, ub0, ub;     // block tokens [0, ua) and [ub0, ub)
+  int ta, tiles;       // tiles of the first range; tiles in all
 };
 
 // Rows' limits: key position j takes part iff j < end && (j < sk || (lb <= j && j <= hi)).
@@ -109,15 +139,161 @@ __device__ __forceinline__ uint32_t visible32(const int *pos, bool blk, int word
   return base == kNever ? 0u : visible(base + 32 * word % PAGE, 32, end, w);
 }
 
+template <bool KV4, int PAGE>
+__device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &first, Limits &last, bool report) {
+  constexpr int PPT = kBN / PAGE;
+  const Shape &sh = prm.sh;
+  const PagedArgs &a = prm.a;
+  Keys ks;
+  const int rt = unit % prm.rowtiles;
+  ks.h = unit / prm.rowtiles % sh.Hkv;
+  ks.s = unit / prm.rowtiles / sh.Hkv;
+  ks.b0 = rt * prm.bpt;
+  ks.n = clamp_prefix(__ldg(a.n_ctx + ks.s), sh.max_pages, PAGE, a.status, report);
+  ks.nb = block_tokens(a.n_new, ks.s, sh.B, a.status, report);
+  const int b_end = min(ks.b0 + prm.bpt, ks.nb);  // the unit's tokens are [b0, b_end)
+  ks.rows = max(0, b_end - ks.b0) * sh.G;
+  first = row_limits<KV4>(a, ks.n, ks.b0);
+  last = row_limits<KV4>(a, ks.n, max(ks.b0, b_end - 1));
+  const int np = (ks.n + PAGE - 1) / PAGE;
+  if (KV4) {
+    ks.nsp = 0;
+    ks.wp0 = 0;
+    ks.npg = np;
+    if (a.idx) {
+      ks.npg = __ldg(a.idx_cnt + (size_t)ks.s * sh.Hkv + ks.h);
+      if (ks.npg < 0 || ks.npg > sh.kmax) {
+        if (report) raise_status(a.status, kStatusBadIndex);
+        ks.npg = max(0, min(ks.npg, sh.kmax));
+      }
+    }
+    ks.ua = 0;
+    ks.ub0 = 0;
+    ks.ub = a.blk_k ? ks.nb : 0;
+  } else {
+    const int lb = max(0, first.lb);  // the lowest position that a window of the unit reaches
+    ks.nsp = (min(min(a.sinks, ks.n), lb) + PAGE - 1) / PAGE;
+    ks.wp0 = max(ks.nsp, lb / PAGE);
+    ks.npg = ks.nsp + max(0, np - ks.wp0);
+    const int ue = a.blk_k ? (a.causal ? min(ks.nb, b_end) : ks.nb) : 0;
+    ks.ua = max(0, min(ue, clamp_int((long long)last.sk - ks.n)));  // sinks that reach into the block
+    ks.ub0 = max(ks.ua, clamp_int((long long)first.lb - ks.n));
+    ks.ub = min(ue, clamp_int((long long)last.hi + 1 - ks.n));
+    if (ks.ub0 >= ks.ub) ks.ub0 = ks.ub = 0;
+  }
+  ks.ta = (ks.ua + kBN - 1) / kBN;
+  const int tb = ks.ta + (ks.ub - ks.ub0 + kBN - 1) / kBN;
+  ks.pt = (ks.npg + PPT - 1) / PPT;
+  if (ks.pt + tb == 0) ks.pt = 1;  // rows without a key: one tile without a page
+  ks.tiles = ks.rows > 0 ? ks.pt + tb : 0;
+  return ks;
+}
+
+// The walk of a CTA through its units; every role walks the same way.
+template <bool KV4, int PAGE>
+struct Walk {
+  const Params &prm;
+  int u, off, left;  // next unit, its first tile, tiles left of the share
+  Keys ks;           // the current piece: tiles [t0, t0 + nt) of its unit
+  Limits first, last;
+  int unit, t0, nt;
+  __device__ __forceinline__ Walk(const Params &p, int u0, int off0, int left0) : prm(p), u(u0), off(off0), left(left0), unit(0), t0(0), nt(0) {}
+  __device__ __forceinline__ bool next(bool report = false) {
+    while (u < prm.units && left > 0) {
+      unit = u;
+      ks = unit_keys<KV4, PAGE>(prm, u, first, last, report);
+      t0 = off;
+      nt = min(ks.tiles - off, left);
+      off = 0;
+      if (prm.shared_out) {
+        left -= nt;
+        ++u;
+      } else {
+        u += gridDim.x;
+      }
+      if (nt > 0) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool begins() const { return t0 == 0; }
+  __device__ __forceinline__ bool ends() const { return t0 + nt == ks.tiles; }
+
+  // Page e of tile t: logical and physical; lp = -1 where the list has ended, phys = -1
+  // where the page cannot be read.
+  __device__ __forceinline__ void page_at(int t, int e, int &lp, int &phys) const {
+    constexpr int PPT = kBN / PAGE;
+    const Shape &sh = prm.sh;
+    const int i = t * PPT + e;
+    lp = -1;
+    phys = -1;
+    if (t >= ks.pt || i >= ks.npg) return;
+    if (KV4 && prm.a.idx) {
+      lp = __ldg(prm.a.idx + ((size_t)ks.s * sh.Hkv + ks.h) * sh.kmax + i);
+      if (lp < 0 || (long long)lp * PAGE >= ks.n) lp = -2;
+    } else {
+      lp = i < ks.nsp ? i : ks.wp0 + (i - ks.nsp);
+    }
+    if (lp >= 0) phys = (int)physical_page(sh, ks.s, lp);
+  }
+  // A page whose every token every row sees.
+  __device__ __forceinline__ bool page_full(int lp, int phys) const {
+    const int pb = lp * PAGE;
+    return phys >= 0 && pb + PAGE <= ks.n && (KV4 || pb + PAGE <= prm.a.sinks || pb >= last.lb);
+  }
+  // First block token of tile t >= pt, where its range ends (a tile of the first range
+  // must not repeat tokens of the second), and whether every row sees all 128.
+  __device__ __forceinline__ int blk_tile(int t, int &u_end, bool &full) const {
+    const int i = t - ks.pt;
+    const bool sink = i < ks.ta;
+    const int u0 = sink ? i * kBN : ks.ub0 + (i - ks.ta) * kBN;
+    const int p0 = ks.n + u0;
+    u_end = sink ? ks.ua : ks.nb;
+    full = u0 + kBN <= u_end && (sink ? p0 + kBN <= first.sk : p0 >= last.lb && p0 + kBN - 1 <= first.hi);
+    return u0;
+  }
+  // Writes the table entry of tile t (a whole warp; lane e < PPT holds page e).
+  __device__ __forceinline__ void put_table(int *tab, int t, int lane, int lp, int phys) const {
+    constexpr int PPT = kBN / PAGE;
+    if (t >= ks.pt) {
+      bool full;
+      int u_end;
+      const int u0 = blk_tile(t, u_end, full);
+      if (lane == 0) {
+        tab[0] = ks.n + u0;
+        tab[8] = (full ? 1 : 0) | 2;
+        tab[9] = ks.n + u_end;
+      }
+    } else {
+      if (lane < PPT && lp != -1 && phys < 0) raise_status(prm.a.status, kStatusBadIndex);
+      if (lane < PPT) tab[lane] = phys >= 0 ? lp * PAGE : kNever;
+      const bool full = __all_sync(0xffffffffu, lane >= PPT || page_full(lp, phys));
+      if (lane == 0) {
+        tab[8] = full ? 1 : 0;
+        tab[9] = ks.n;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, int PAGE, bool KV4>
 __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     paged_attn(const __grid_constant__ Params prm, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-               const __grid_constant__ CUtensorMap kmap4, const __grid_constant__ CUtensorMap vmap4,
                const __grid_constant__ CUtensorMap bkmap, const __grid_constant__ CUtensorMap bvmap) {
   using C = Cfg<D, KV4>;
   constexpr int ST = C::kStages;
-  constexpr int PPT = kBN / PAGE;  // pages of a tile
+  constexpr int PPT = kBN / PAGE;      // pages of a tile
+  constexpr bool kBoxes = PAGE >= 64;  // bf16 pages come by TMA
+  constexpr uint32_t kLoaders = KV4 ? 64 : 32;  // threads that fill K, and that fill V
   extern __shared__ unsigned char smem_raw[];
   const Shape &sh = prm.sh;
   const PagedArgs &a = prm.a;
@@ -130,47 +306,54 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   auto k_empty = [&](int st) { return bar(ST + st); };
   auto v_full = [&](int st) { return bar(2 * ST + st); };
   auto v_empty = [&](int st) { return bar(3 * ST + st); };
-  auto s_full = [&](int g) { return bar(4 * ST + g); };
-  auto p_full = [&](int g) { return bar(4 * ST + 2 + g); };
-  auto pv_done = [&](int g) { return bar(4 * ST + 4 + g); };
-  const uint32_t q_full = bar(4 * ST + 6), drain = bar(4 * ST + 7);
-  auto table = [&](int st) { return reinterpret_cast<int *>(smem + C::kOffTab + st * 48); };
+  auto tab_full = [&](int k) { return bar(4 * ST + k % kTabs); };
+  constexpr int kB0 = 4 * ST + kTabs;
+  auto s_full = [&](int k) { return bar(kB0 + k % 3); };
+  auto p_full = [&](int k) { return bar(kB0 + 3 + k % 3); };
+  auto pv_done = [&](int k) { return bar(kB0 + 6 + (k & 1)); };
+  auto decided = [&](int k) { return bar(kB0 + 8 + (k & 1)); };
+  const uint32_t q_full = bar(kB0 + 10), q_empty = bar(kB0 + 11), o_full = bar(kB0 + 12), o_free = bar(kB0 + 13);
+  // softmax threads among themselves, the loaders of K and of V among themselves (4-bit cache), the last MMA
+  const uint32_t meet = bar(kB0 + 14), drain = bar(kB0 + 17);
+  auto loaders = [&](bool isv) { return bar(kB0 + 15 + (isv ? 1 : 0)); };
+  auto table = [&](int k) { return reinterpret_cast<int *>(smem + C::kOffTab + (k % kTabs) * 40); };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+  int *scan = reinterpret_cast<int *>(smem + C::kOffMisc + 8);  // first unit, its first tile, tiles of the share
+  float *m_ref = reinterpret_cast<float *>(smem + C::kOffM), *l_x = reinterpret_cast<float *>(smem + C::kOffL);
   const WaitCtx ctx{abort_flag, a.status};
   volatile int never = 0;
   const WaitCtx drain_ctx{&never, a.status};
-
-  // unit: (sequence, KV head, row tile, split)
-  const int sp = blockIdx.x % prm.splits;
-  const int unit = blockIdx.x / prm.splits;
-  const int rt = unit % prm.rowtiles;
-  const int h = unit / prm.rowtiles % sh.Hkv;
-  const int s = unit / prm.rowtiles / sh.Hkv;
-  const int b0 = rt * prm.bpt;
-  const int rows_max = min(prm.bpt, sh.B - b0) * sh.G;  // before n_new
-  const int active_warps = (rows_max + 31) / 32;        // of each softmax group
+  const int aw = (prm.bpt * sh.G + 31) / 32;  // warps of a group that hold rows; the others rest
 
   if (threadIdx.x == 0) {
     for (int st = 0; st < ST; ++st) {
-      mbar_init(k_full(st), KV4 ? 128 : 1);
+      mbar_init(k_full(st), kLoaders);
       mbar_init(k_empty(st), 1);
-      mbar_init(v_full(st), KV4 ? 128 : 1);
+      mbar_init(v_full(st), kLoaders);
       mbar_init(v_empty(st), 1);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(s_full(g), 1);
-      mbar_init(p_full(g), 32 * active_warps);
-      mbar_init(pv_done(g), 1);
+    for (int k = 0; k < kTabs; ++k) mbar_init(tab_full(k), 1);
+    for (int k = 0; k < 3; ++k) {
+      mbar_init(s_full(k), 1);
+      mbar_init(p_full(k), 32 * aw);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(pv_done(k), 1);
+      mbar_init(decided(k), 32 * aw);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 64 * aw);
+    mbar_init(meet, 64 * aw);
+    mbar_init(loaders(false), 64);
+    mbar_init(loaders(true), 64);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    scan[0] = prm.units;
+    scan[1] = scan[2] = 0;
     fence_mbar_init();
     tma_prefetch_map(&qmap);
-    if (!KV4) {
-      tma_prefetch_map(&kmap);
-      tma_prefetch_map(&vmap);
-    }
   }
   if (warp == 1) {
     tmem_alloc(base + C::kOffMisc, C::kTmemCols);
@@ -179,292 +362,247 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  // ---- the keys of this row tile, and this split's tiles of them
-  const bool reporter = threadIdx.x == 0 && h == 0 && rt == 0 && sp == 0;
-  Keys ks;
-  ks.n = clamp_prefix(a.n_ctx[s], sh.max_pages, PAGE, a.status, reporter);
-  ks.nb = block_tokens(a.n_new, s, sh.B, a.status, reporter);
-  const int b_end = min(b0 + prm.bpt, ks.nb);  // this tile's tokens are [b0, b_end)
-  const int rows = max(0, b_end - b0) * sh.G;
-  const int32_t *idx_head = nullptr;
-  Limits first = row_limits<KV4>(a, ks.n, b0), last = row_limits<KV4>(a, ks.n, max(b0, b_end - 1));
-  {
-    const int np = (ks.n + PAGE - 1) / PAGE;
-    if (KV4) {
-      ks.nsp = 0;
-      ks.wp0 = 0;
-      ks.npg = np;
-      if (a.idx) {
-        idx_head = a.idx + ((size_t)s * sh.Hkv + h) * sh.kmax;
-        ks.npg = a.idx_cnt[(size_t)s * sh.Hkv + h];
-        if (ks.npg < 0 || ks.npg > sh.kmax) {
-          if (threadIdx.x == 0 && rt == 0 && sp == 0) raise_status(a.status, kStatusBadIndex);
-          ks.npg = max(0, min(ks.npg, sh.kmax));
-        }
+  // ---- this CTA's share: a scan over the units' tiles
+  if (prm.shared_out) {
+    int *sums = reinterpret_cast<int *>(m_ref);  // of the warps
+    const int u0 = threadIdx.x * kUnitsPerThread;
+    int cnt[kUnitsPerThread], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kUnitsPerThread; ++i) {
+      cnt[i] = 0;
+      if (u0 + i < prm.units) {
+        Limits x, y;
+        cnt[i] = unit_keys<KV4, PAGE>(prm, u0 + i, x, y, blockIdx.x == 0).tiles;
       }
-      ks.ua = 0;
-      ks.ub0 = 0;
-      ks.ub = a.blk_k ? ks.nb : 0;
-    } else {
-      const int lb = max(0, first.lb);  // the lowest position that a window of the tile reaches
-      ks.nsp = (min(min(a.sinks, ks.n), lb) + PAGE - 1) / PAGE;
-      ks.wp0 = max(ks.nsp, lb / PAGE);
-      ks.npg = ks.nsp + max(0, np - ks.wp0);
-      const int ue = a.blk_k ? (a.causal ? min(ks.nb, b_end) : ks.nb) : 0;
-      ks.ua = max(0, min(ue, clamp_int((long long)last.sk - ks.n)));  // sinks that reach into the block
-      ks.ub0 = max(ks.ua, clamp_int((long long)first.lb - ks.n));
-      ks.ub = min(ue, clamp_int((long long)last.hi + 1 - ks.n));
-      if (ks.ub0 >= ks.ub) ks.ub0 = ks.ub = 0;
+      mine += cnt[i];
     }
-    ks.pt = (ks.npg + PPT - 1) / PPT;
-    ks.ta = (ks.ua + kBN - 1) / kBN;
-    ks.tiles = rows > 0 ? ks.pt + ks.ta + (ks.ub - ks.ub0 + kBN - 1) / kBN : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      before += w < warp ? sums[w] : 0;
+      total += sums[w];
+    }
+    const int shares = max(1, min((int)gridDim.x, total / kMinTiles));
+    const int c = blockIdx.x;
+    if (c < shares) {
+      const int lo = (int)((long long)total * c / shares), hi = (int)((long long)total * (c + 1) / shares);
+      int at = before + upto - mine;  // first tile of this thread's units
+#pragma unroll
+      for (int i = 0; i < kUnitsPerThread; ++i) {
+        if (lo >= at && lo < at + cnt[i]) {
+          scan[0] = u0 + i;
+          scan[1] = lo - at;
+          scan[2] = hi - lo;
+        }
+        at += cnt[i];
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    scan[0] = blockIdx.x;
+    scan[2] = INT_MAX;
   }
-  const int t0 = (int)((long long)ks.tiles * sp / prm.splits);
-  const int nt = (int)((long long)ks.tiles * (sp + 1) / prm.splits) - t0;
-  const int pend = ks.n;
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);
+  Walk<KV4, PAGE> walk(prm, scan[0], scan[1], scan[2]);
 
-  // page e of tile t (both counted from the list's start): logical and physical
-  auto page_at = [&](int t, int e, int &lp, int &phys) {
-    const int i = t * PPT + e;
-    lp = -1;
-    phys = -1;
-    if (t >= ks.pt || i >= ks.npg) return;
-    if (KV4 && idx_head) {
-      lp = idx_head[i];
-      if (lp < 0 || (long long)lp * PAGE >= ks.n) lp = -2;
-    } else {
-      lp = i < ks.nsp ? i : ks.wp0 + (i - ks.nsp);
-    }
-    if (lp >= 0) phys = (int)physical_page(sh, s, lp);
-  };
-  // a page whose every token every row sees
-  auto page_full = [&](int lp, int phys) {
-    const int pb = lp * PAGE;
-    return phys >= 0 && pb + PAGE <= pend && (KV4 || pb + PAGE <= a.sinks || pb >= last.lb);
-  };
-  // first block token of tile t >= pt, where its range ends (a tile of the first range must
-  // not repeat tokens of the second), and whether every row sees all 128
-  auto blk_tile = [&](int t, int &u_end, bool &full) {
-    const int i = t - ks.pt;
-    const bool sink = i < ks.ta;
-    const int u0 = sink ? i * kBN : ks.ub0 + (i - ks.ta) * kBN;
-    const int p0 = ks.n + u0;
-    u_end = sink ? ks.ua : ks.nb;
-    full = u0 + kBN <= u_end && (sink ? p0 + kBN <= first.sk : p0 >= last.lb && p0 + kBN - 1 <= first.hi);
-    return u0;
-  };
-
-  float m_used = -INFINITY, l = 0.f;
-  bool alive = true;
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer --
-    if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(q_full, (uint32_t)min(prm.bpt, sh.B) * sh.G * 128u * C::kHalves);
-      for (int hf = 0; hf < C::kHalves; ++hf)
-        tma_load_3d(base + C::kOffQ + hf * C::kHalf, &qmap, q_full, hf * 64, h * sh.G, s * sh.B + b0);
-    }
-    __syncwarp();
-    if (!KV4) {
-      int issued_k = 0, issued_v = 0;
-      int lp = -1, phys = -1;
-      if (nt > 0 && lane < PPT) page_at(t0, lane, lp, phys);
-      for (int k = 0; k < nt; ++k) {
-        const int st = k % ST, t = t0 + k;
-        int lp1 = -1, phys1 = -1;  // the next tile's pages, fetched before this tile's waits
-        if (k + 1 < nt && lane < PPT) page_at(t + 1, lane, lp1, phys1);
-        const uint32_t sk = base + C::kOffK + st * C::kTile, sv = base + C::kOffV + st * C::kTile;
-        const bool blk = t >= ks.pt;
-        bool full = false;
-        int u0 = 0, u_end = 0, nvalid = 0;
-        bool run = false;
-        if (blk) {
-          u0 = blk_tile(t, u_end, full);
-        } else {
-          const bool listed = lane < PPT && lp != -1;
-          if (listed && phys < 0) raise_status(a.status, kStatusBadIndex);
-          nvalid = __popc(__ballot_sync(0xffffffffu, listed && phys >= 0));
-          full = __all_sync(0xffffffffu, lane >= PPT || page_full(lp, phys)) && nvalid == PPT;
-          const int p0 = __shfl_sync(0xffffffffu, phys, 0);
-          run = nvalid == PPT && __all_sync(0xffffffffu, lane >= PPT || phys == p0 + lane);
-        }
-        const uint32_t bytes = (blk ? (uint32_t)prm.box_blk : (uint32_t)nvalid * PAGE) * 128u * C::kHalves;
-        auto load = [&](uint32_t dst, uint32_t br, const CUtensorMap *m2, const CUtensorMap *m4, const CUtensorMap *mb) {
-          if (lane == 0) mbar_arrive_expect_tx(br, bytes);
-          __syncwarp();
-          if (blk) {
-            if (lane < C::kHalves) tma_load_3d(dst + lane * C::kHalf, mb, br, lane * 64, h, s * sh.B + u0);
-          } else if (run) {
-            const int p0 = __shfl_sync(0xffffffffu, phys, 0);
-            if (lane < C::kHalves) tma_load_4d(dst + lane * C::kHalf, m4, br, lane * 64, 0, h, p0);
-          } else {
-            const int e = lane % PPT, hf = lane / PPT;
-            const int ph = __shfl_sync(0xffffffffu, phys, e);
-            if (hf < C::kHalves && ph >= 0)
-              tma_load_2d(dst + hf * C::kHalf + e * PAGE * 128u, m2, br, hf * 64,
-                          (int)(((long long)ph * sh.Hkv + h) * PAGE));
-          }
-        };
-        if (k >= ST && !__all_sync(0xffffffffu, mbar_wait(k_empty(st), ((k / ST) - 1) & 1, ctx))) break;
-        load(sk, k_full(st), &kmap, &kmap4, &bkmap);
-        issued_k = k + 1;
-        if (k >= ST && !__all_sync(0xffffffffu, mbar_wait(v_empty(st), ((k / ST) - 1) & 1, ctx))) break;
-        int *tab = table(st);
-        if (blk) {
-          if (lane == 0) tab[0] = ks.n + u0;
-        } else if (lane < PPT) {
-          tab[lane] = phys >= 0 ? lp * PAGE : kNever;
-        }
-        if (lane == 0) {
-          tab[8] = (full ? 1 : 0) | (blk ? 2 : 0);
-          tab[9] = blk ? ks.n + u_end : ks.n;
-        }
-        __syncwarp();
-        load(sv, v_full(st), &vmap, &vmap4, &bvmap);
-        issued_v = k + 1;
-        lp = lp1;
-        phys = phys1;
+  // Parity waits.  A wait names one of a barrier's phases, and must be made when the
+  // phase before it has completed and the one after it cannot have.  k counts the CTA's
+  // tiles over all its units.
+  //   k_full, v_full (k)   the stage's next fill follows k_empty / v_empty of tile k,
+  //                        committed after the MMAs that follow the issuer's wait.  Softmax
+  //                        threads wait for v_full(k) before P(k), which PV(k) follows.
+  //   k_empty, v_empty     a stage's next commit needs the fill that follows the wait.
+  //   tab_full (k)         slot k's next fill is tile k + 8; its loader has waited for S of
+  //                        tile k + 8 - ST, k + 3 at the least, which needs PV(k), so P(k).
+  //   s_full, p_full (k)   three of each: S(k + 3) is sent after PV(k), P(k + 3) follows it.
+  //   pv_done (k)          two, alternating: the issuer waits for PV(k) before S(k + 3), when
+  //                        PVs up to k are out.  A softmax thread waits for PV(k - 1) before
+  //                        it decides tile k; PV(k + 1) needs that decision, and PV(k - 3)
+  //                        was done before S(k) was sent.
+  //   decided (k)          two: the group of tile k + 1 waits for it unless a unit begins
+  //                        there; the next one, k + 2, needs the decision on k + 1.  Before
+  //                        a unit both groups have met after the last PV, so none is skipped
+  //                        that has not completed.
+  //   q_full, q_empty, o_full, o_free   once per unit, each after the one before it.
+  if (KV4 ? warp == 0 : warp == 11) {
+    // ---------------------------------------------------------------- queries --
+    int it = 0;
+    if (lane == 0) {
+      while (walk.next(!prm.shared_out)) {  // (the scan has reported bad lengths)
+        if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, ctx)) break;
+        mbar_arrive_expect_tx(q_full, (uint32_t)prm.bpt * sh.G * 128u * C::kHalves);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(base + C::kOffQ + hf * C::kHalf, &qmap, q_full, hf * 64, walk.ks.h * sh.G, walk.ks.s * sh.B + walk.ks.b0);
+        ++it;
       }
-      // copies in flight land before the CTA's shared memory is released
-      if (lane == 0) {
-        for (int k = max(0, issued_k - ST); k < issued_k; ++k) mbar_wait(k_full(k % ST), (k / ST) & 1, drain_ctx);
-        for (int k = max(0, issued_v - ST); k < issued_v; ++k) mbar_wait(v_full(k % ST), (k / ST) & 1, drain_ctx);
-      }
+      if (it > 0) mbar_wait(q_full, (it - 1) & 1, drain_ctx);  // a copy in flight lands before the CTA ends
     }
-    if (lane == 0 && nt > 0) mbar_wait(q_full, 0, drain_ctx);
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer --
-    // Every parity wait below is on the barrier's current or just completed phase:
-    // a stage is refilled only after the commit that frees it, which follows the wait
-    // for its fill; S of a group's next tile is sent after the wait for P of its last
-    // one, and pv_done(g) is waited for once per phase, right where the S follows.
-    if (lane == 0 && nt > 0) {
+    if (lane == 0) {
       constexpr uint32_t ids = idesc_bf16(128, kBN, false, false);
       constexpr uint32_t ido = idesc_bf16(128, D, false, true);
-      auto issue_s = [&](int j) {
-        const int st = j % ST, g = j & 1;
-        if (!mbar_wait(k_full(st), (j / ST) & 1, ctx)) return false;
-        // P of this group's previous tile lies in the same columns: its PV must be done
-        if (j >= 2 && !mbar_wait(pv_done(g), ((j >> 1) - 1) & 1, ctx)) return false;
+      Walk<KV4, PAGE> ahead = walk;  // two tiles ahead: S
+      int s_it = -1, s_left = 0, ks = 0;
+      bool more = true, ok = true;
+      // S of the next tile of the walk, if there is one
+      auto issue_s = [&]() {
+        if (s_left == 0) {
+          more = more && ahead.next();
+          if (!more) return true;
+          s_left = ahead.nt;
+          ++s_it;
+          if (!mbar_wait(q_full, s_it & 1, ctx)) return false;
+        }
+        const int st = ks % ST;
+        if (!mbar_wait(k_full(st), (ks / ST) & 1, ctx)) return false;
+        // P of tile ks - 3 lies in the same columns: its PV must be done
+        if (ks >= 3 && !mbar_wait(pv_done(ks - 3), ((ks - 3) >> 1) & 1, ctx)) return false;
         tc_fence_after();
         const uint32_t sk = base + C::kOffK + st * C::kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + g * kBN, sdesc_sw128(base + C::kOffQ + off, 16, 1024), sdesc_sw128(sk + off, 16, 1024), ids,
+          const uint32_t at = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+          umma_bf16(tmem + (ks % 3) * kBN, sdesc_sw128(base + C::kOffQ + at, 16, 1024), sdesc_sw128(sk + at, 16, 1024), ids,
                     kk > 0 ? 1u : 0u);
         }
-        umma_commit(s_full(g));
+        umma_commit(s_full(ks));
         umma_commit(k_empty(st));
+        ++ks;
+        if (--s_left == 0) umma_commit(q_empty);
         return true;
       };
-      bool ok = mbar_wait(q_full, 0, ctx);
-      for (int j = 0; ok && j < 2 && j < nt; ++j) ok = issue_s(j);
-      for (int j = 0; ok && j < nt; ++j) {
-        const int st = j % ST, g = j & 1;
-        if (!mbar_wait(p_full(g), (j >> 1) & 1, ctx)) break;
-        if (!mbar_wait(v_full(st), (j / ST) & 1, ctx)) break;
-        tc_fence_after();
-        const uint32_t sv = base + C::kOffV + st * C::kTile;
+      ok = issue_s() && issue_s();
+      int k = 0;
+      for (int it = 0; ok && walk.next(); ++it) {
+        for (int j = 0; ok && j < walk.nt; ++j, ++k) {
+          const int st = k % ST;
+          ok = issue_s() && mbar_wait(p_full(k), (k / 3) & 1, ctx) && mbar_wait(v_full(st), (k / ST) & 1, ctx);
+          // the epilogue of the unit before has read O
+          if (ok && j == 0 && it > 0) ok = mbar_wait(o_free, (it - 1) & 1, ctx);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sv = base + C::kOffV + st * C::kTile;
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_bf16_ts(tmem + C::kTmemO + g * D, tmem + g * kBN + kk * 8, sdesc_sw128(sv + kk * 16 * 128, C::kHalf, 1024),
-                       ido, (j > 1 || kk > 0) ? 1u : 0u);
-        umma_commit(pv_done(g));
-        umma_commit(v_empty(st));
-        if (j + 2 < nt) ok = issue_s(j + 2);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            umma_bf16_ts(tmem + C::kTmemO, tmem + (k % 3) * kBN + kk * 8, sdesc_sw128(sv + kk * 16 * 128, C::kHalf, 1024), ido,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(pv_done(k));
+          umma_commit(v_empty(st));
+        }
+        if (ok) umma_commit(o_full);
       }
-      umma_commit(drain);  // every issued MMA completes before TMEM is released
+      umma_commit(drain);  // every issued MMA completes before TMEM and the tiles are released
       mbar_wait(drain, 0, drain_ctx);
     }
     __syncwarp();
-  } else if (warp < 10) {
+  } else if (warp >= 2 && warp < 10) {
     // ---------------------------------------------------------- softmax groups --
     const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    // the quarters of TMEM's lanes that hold rows; the other warps have nothing to do
-    if (quarter < active_warps) {
+    if (quarter < aw) {
       const uint32_t lt = tmem + ((uint32_t)(quarter * 32) << 16);
-      const uint32_t sc = lt + g * kBN, oc = lt + C::kTmemO + g * D;
-      const Limits mine = row_limits<KV4>(a, ks.n, b0 + r / sh.G);
-      Limits all;  // keys that some row of the tile may see
-      all.lb = first.lb;
-      all.hi = last.hi;
-      all.sk = last.sk;
-      int m = 0;  // tiles this group has finished
-      for (int k = g; k < nt; k += 2, ++m) {
-        const int st = k % ST;
-        alive = __all_sync(0xffffffffu, mbar_wait(s_full(g), m & 1, ctx));
-        // the tile's table, and V for the rows zeroed below (its stage is refilled only
-        // after this tile's P)
-        alive = alive && __all_sync(0xffffffffu, mbar_wait(v_full(st), (k / ST) & 1, ctx));
-        if (!alive) break;
-        tc_fence_after();
-        const int *tab = table(st);
-        const int flags = tab[8];
-        const bool blk = flags & 2;
-        const int end = tab[9];
-        uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!(flags & 1)) {
+      const uint32_t oc = lt + C::kTmemO;
+      bool alive = true;
+      int k0 = 0, it = 0, met = 0;  // first tile of the unit, units done, meetings
+      // all softmax threads; a bounded wait, unlike a named barrier
+      auto meet_all = [&]() {
+        mbar_arrive(meet);
+        alive = __all_sync(0xffffffffu, mbar_wait(meet, met & 1, ctx));
+        ++met;
+        return alive;
+      };
+      if (prm.shared_out && warp == 2 + ((4 - 2) & 3) && lane == 0) {  // the warp of group 0 with row 0
+        prm.piece[2 * blockIdx.x].unit = -1;
+        prm.piece[2 * blockIdx.x + 1].unit = -1;
+      }
+      for (; alive && walk.next(); ++it) {
+        const Keys &ks = walk.ks;
+        const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
+        const Limits all{walk.first.lb, walk.last.hi, walk.last.sk};  // keys that some row may see
+        float m_used = -INFINITY, l = 0.f;
+        const int k1 = k0 + walk.nt;
+        for (int k = k0 + ((k0 ^ g) & 1); k < k1; k += 2) {
+          const uint32_t sc = lt + (k % 3) * kBN;
+          alive = __all_sync(0xffffffffu, mbar_wait(tab_full(k), (k / kTabs) & 1, ctx) && mbar_wait(s_full(k), (k / 3) & 1, ctx));
+          if (!alive) break;
+          tc_fence_after();
+          const int *tab = table(k);
+          const int flags = tab[8];
+          uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!(flags & 1)) {
+            const bool blk = flags & 2;
+            const int end = tab[9], st = k % ST;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) bits[w] = visible32<PAGE>(tab, blk, w, end, mine);
-          // value rows that no row of the tile sees are zeroed: 0 * stale data must not reach O
-          for (int key = quarter * 32 + lane; key < kBN; key += 32 * active_warps) {
-            const uint32_t any = visible32<PAGE>(tab, blk, key >> 5, end, all);
-            if ((any >> (key & 31)) & 1u) continue;
-            unsigned char *row = smem + C::kOffV + st * C::kTile + key * 128;
+            for (int w = 0; w < 4; ++w) bits[w] = visible32<PAGE>(tab, blk, w, end, mine);
+            // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
+            alive = __all_sync(0xffffffffu, mbar_wait(v_full(st), (k / ST) & 1, ctx));
+            if (!alive) break;
+            for (int key = quarter * 32 + lane; key < kBN; key += 32 * aw) {
+              const uint32_t any = visible32<PAGE>(tab, blk, key >> 5, end, all);
+              if ((any >> (key & 31)) & 1u) continue;
+              unsigned char *row = smem + C::kOffV + st * C::kTile + key * 128;
 #pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
+              for (int hf = 0; hf < C::kHalves; ++hf)
 #pragma unroll
-              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + hf * C::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + hf * C::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
-        }
-        // The row's scores, all 128 in registers; with the 4-bit cache's warps beside it a
-        // thread has 128 registers: it holds the first 64, and reads the others twice.
-        constexpr int kHold = KV4 ? 64 : 128;
-        uint32_t x[kHold];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (KV4) {
-          tmem_ld64(sc, x);
-        } else {
-          tmem_ld64x2(sc, *reinterpret_cast<uint32_t(*)[64]>(&x[0]), sc + 64, *reinterpret_cast<uint32_t(*)[64]>(&x[64]));
-        }
-        auto hide = [&](uint32_t *y, int w) {  // scores of 32 keys that take no part: -inf
-          if (bits[w] == ~0u) return;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!((bits[w] >> j) & 1u)) y[j] = 0xff800000u;
-        };
-#pragma unroll
-        for (int w = 0; w < kHold / 32; ++w) hide(x + 32 * w, w);
-#pragma unroll
-        for (int j = 0; j < kHold; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
-        if constexpr (KV4) {
-#pragma unroll
-          for (int w = 2; w < 4; ++w) {
-            uint32_t y[32];
-            tmem_ld32(sc + 32 * w, y);
-            hide(y, w);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(y[j]));
+          // The row's scores, all 128 in registers; with the 4-bit cache's warps beside it a
+          // thread has 128 registers: it holds the first 64, and reads the others twice.
+          constexpr int kHold = KV4 ? 64 : 128;
+          uint32_t x[kHold];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if constexpr (KV4) {
+            tmem_ld64(sc, x);
+          } else {
+            tmem_ld64x2(sc, *reinterpret_cast<uint32_t(*)[64]>(&x[0]), sc + 64, *reinterpret_cast<uint32_t(*)[64]>(&x[64]));
           }
-        }
-        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2;
-        const bool need = tmax > m_used + kRescaleLog2 || (m_used == -INFINITY && tmax > -INFINITY);
-        if (__any_sync(0xffffffffu, need)) {
-          float alpha = 1.f;
-          if (need) {
-            alpha = m_used == -INFINITY ? 0.f : fast_exp2(m_used - tmax);
-            m_used = tmax;
-            l *= alpha;
+          auto hide = [&](uint32_t *y, int w) {  // scores of 32 keys that take no part: -inf
+            if (bits[w] == ~0u) return;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((bits[w] >> j) & 1u)) y[j] = 0xff800000u;
+          };
+#pragma unroll
+          for (int w = 0; w < kHold / 32; ++w) hide(x + 32 * w, w);
+#pragma unroll
+          for (int j = 0; j < kHold; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+          if constexpr (KV4) {
+#pragma unroll
+            for (int w = 2; w < 4; ++w) {
+              uint32_t y[32];
+              tmem_ld32(sc + 32 * w, y);
+              hide(y, w);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(y[j]));
+            }
           }
-          if (m > 0) {  // PV of the group's previous tile is done: this tile's S was sent after it
+          const float tmax = r < ks.rows ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2 : -INFINITY;
+          // the reference so far, from the group of the tile before; a row past the unit's keeps none
+          float m_prev = -INFINITY;
+          if (k > k0) {
+            alive = __all_sync(0xffffffffu, mbar_wait(decided(k - 1), ((k - 1) >> 1) & 1, ctx));
+            if (!alive) break;
+            m_prev = m_ref[r];
+          }
+          const bool need = tmax > m_prev + kRescaleLog2 || (m_prev == -INFINITY && tmax > -INFINITY);
+          const float m_now = need ? tmax : m_prev;
+          if (k > k0 && __any_sync(0xffffffffu, need)) {  // O holds the unit's earlier tiles
+            alive = __all_sync(0xffffffffu, mbar_wait(pv_done(k - 1), ((k - 1) >> 1) & 1, ctx));
+            if (!alive) break;
+            tc_fence_after();
+            const float alpha = !need ? 1.f : m_prev == -INFINITY ? 0.f : fast_exp2(m_prev - m_now);
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o[32];
@@ -473,234 +611,304 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
               tmem_st32(oc + c0, o);
             }
+            tc_fence_before();
           }
+          if (need || k == k0) m_ref[r] = m_now;
+          mbar_arrive(decided(k));
+          if (m_now != m_used) {
+            l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - m_now);
+            m_used = m_now;
+          }
+          const float mu = m_used == -INFINITY ? 0.f : m_used;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 scale2 = make_float2(sh.sl2, sh.sl2), mu2 = make_float2(-mu, -mu);
+          auto emit = [&](const uint32_t *y, int w) {  // 32 probabilities, over S columns already read
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 e = fma2(make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), scale2, mu2);
+              const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              sum[j & 1] = add2(sum[j & 1], p);
+              pk[j] = pack_bf16x2(p.x, p.y);
+            }
+            tmem_st16_async(sc + 16 * w, pk);
+          };
+#pragma unroll
+          for (int w = 0; w < kHold / 32; ++w) emit(x + 32 * w, w);
+          if constexpr (KV4) {
+            tmem_ld64(sc + 64, x);
+#pragma unroll
+            for (int w = 2; w < 4; ++w) {
+              hide(x + 32 * (w - 2), w);
+              emit(x + 32 * (w - 2), w);
+            }
+          }
+          tmem_wait_st();
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tc_fence_before();
+          mbar_arrive(p_full(k));
         }
-        const float mu = m_used == -INFINITY ? 0.f : m_used;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 scale2 = make_float2(sh.sl2, sh.sl2), mu2 = make_float2(-mu, -mu);
-        auto emit = [&](const uint32_t *y, int w) {  // 32 probabilities, over S columns already read
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 e = fma2(make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), scale2, mu2);
-            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            sum[j & 1] = add2(sum[j & 1], p);
-            pk[j] = pack_bf16x2(p.x, p.y);
-          }
-          tmem_st16_async(sc + 16 * w, pk);
-        };
-#pragma unroll
-        for (int w = 0; w < kHold / 32; ++w) emit(x + 32 * w, w);
-        if constexpr (KV4) {
-          tmem_ld64(sc + 64, x);
-#pragma unroll
-          for (int w = 2; w < 4; ++w) {
-            hide(x + 32 * (w - 2), w);
-            emit(x + 32 * (w - 2), w);
-          }
-        }
-        tmem_wait_st();
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tc_fence_before();
-        mbar_arrive(p_full(g));
-      }
-      if (alive && m > 0) {  // the issuer's one commit after its last MMA
-        alive = __all_sync(0xffffffffu, mbar_wait(drain, 0, ctx));
+        if (!alive) break;
+        // ---- the unit's rows: both groups' sums on the common reference, O from TMEM, a
+        //      group per half of the columns
+        alive = __all_sync(0xffffffffu, mbar_wait(o_full, it & 1, ctx));
+        if (!alive) break;
         tc_fence_after();
-      }
-      if (!alive || m == 0) l = 0.f;
-    }
-  } else if (KV4) {
-    // ------------------------------------------- packed rows into bf16 tiles --
-    // 128 threads; chunk i of a thread is the 16 bytes (32 values, one scale) of group
-    // tid % GR of key 128 / CH * i + tid / GR.  The packed rows of the next tile are
-    // loaded before this tile's stage is waited for, its page ids one tile earlier.
-    constexpr int GR = D / kKv4Group;  // groups of a row
-    constexpr int CH = GR;             // chunks of a thread: 128 * GR / 128
-    const int tid = threadIdx.x - 320;
-    const int grp = tid % GR;
-    struct Raw {
-      uint4 k[CH], v[CH];
-      __nv_bfloat16 ks[CH], vs[CH];
-    };
-    auto key_of = [&](int i) { return i * (kBN / CH) + tid / GR; };
-    auto ids_of = [&](int t, int (&lp)[CH], int (&phys)[CH]) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) page_at(t, key_of(i) / PAGE, lp[i], phys[i]);
-    };
-    auto on = [&](int i, const int (&lp)[CH], const int (&phys)[CH]) {
-      return phys[i] >= 0 && lp[i] * PAGE + key_of(i) % PAGE < pend;
-    };
-    auto fetch = [&](Raw &x, const int (&lp)[CH], const int (&phys)[CH]) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        if (!on(i, lp, phys)) continue;
-        const long long row = ((long long)phys[i] * sh.Hkv + h) * PAGE + key_of(i) % PAGE;
-        x.k[i] = __ldg(reinterpret_cast<const uint4 *>(a.kv4.k + row * (D / 2)) + grp);
-        x.ks[i] = a.kv4.ks[row * GR + grp];
-        x.v[i] = __ldg(reinterpret_cast<const uint4 *>(a.kv4.v + row * (D / 2)) + grp);
-        x.vs[i] = a.kv4.vs[row * GR + grp];
-      }
-    };
-    auto put = [&](uint32_t off, const uint4 (&w)[CH], const __nv_bfloat16 (&sc)[CH], const int (&lp)[CH], const int (&phys)[CH]) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int key = key_of(i);
-        unsigned char *dst = smem + off + (grp / 2) * C::kHalf;
-        const bool o = on(i, lp, phys);
-        __nv_bfloat162 s8, m24;
-        kv4_constants(sc[i], s8, m24);
-        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint4 y = make_uint4(0, 0, 0, 0);
-          if (o) y = make_uint4(kv4_pair(ww[c], 0, s8, m24), kv4_pair(ww[c], 1, s8, m24), kv4_pair(ww[c], 2, s8, m24), kv4_pair(ww[c], 3, s8, m24));
-          *reinterpret_cast<uint4 *>(dst + sw128_offset(key, (grp % 2) * 4 + c)) = y;
+        if (!meet_all()) break;  // m_ref is final
+        const float M = m_ref[r];
+        if (m_used != M) l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
+        if (g == 1) l_x[r] = l;
+        if (!meet_all()) break;
+        if (g == 0) l_x[r] = l = l + l_x[r];
+        if (!meet_all()) break;
+        const float L = g == 0 ? l : l_x[r];
+        const bool has = L != 0.f;  // a NaN sum counts
+        const bool whole = walk.begins() && walk.ends();
+        const int slot = 2 * blockIdx.x + (walk.begins() ? 1 : 0);
+        const bool mine_row = r < ks.rows;
+        const size_t orow = ((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G;
+        const size_t prow = (size_t)slot * ((size_t)prm.bpt * sh.G) + r;
+        const float wt = whole ? (has ? 1.f / L : 0.f) : 1.f;
+        if (g == 0 && mine_row) {
+          if (!whole) {
+            prm.part_ml[prow] = make_float2(M, L);
+          } else if (sh.lse_out) {
+            sh.lse_out[orow] = has ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          }
         }
+        if (!whole && warp == 4 && lane == 0) prm.piece[slot] = Piece{walk.unit, walk.begins(), walk.ends(), 0};
+#pragma unroll
+        for (int i0 = 0; i0 < D / 2; i0 += 32) {
+          const int c0 = g * (D / 2) + i0;
+          uint32_t o[32];
+          tmem_ld32(oc + c0, o);
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = has ? __uint_as_float(o[i]) * wt : 0.f;
+          if (mine_row && whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.o_out + orow * D + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                  pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+          } else if (mine_row) {
+            float4 *dst = reinterpret_cast<float4 *>(prm.part_o + prow * D + c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+          __syncwarp();  // the TMEM loads are warp-collective
+        }
+        tc_fence_before();
+        mbar_arrive(o_free);
+        k0 = k1;
       }
-    };
-    Raw cur, nxt;
-    int lp0[CH], ph0[CH], lp1[CH], ph1[CH];
-    int issued = 0;
+    }
+  } else if (!KV4) {
+    // ------------------------------------------------- bf16 tiles: K or V --
+    const bool isv = warp == 10;
+    const CUtensorMap *map = isv ? &vmap : &kmap, *bmap = isv ? &bvmap : &bkmap;
+    const __nv_bfloat16 *cache = isv ? a.v : a.k;
+    auto full = [&](int st) { return isv ? v_full(st) : k_full(st); };
+    auto empty = [&](int st) { return isv ? v_empty(st) : k_empty(st); };
+    const uint32_t ring = base + (isv ? C::kOffV : C::kOffK);
+    int k = 0, told = 0;  // tiles issued; tiles announced (copies by threads are, one tile late)
     bool ok = true;
-    if (nt > 0) {
-      ids_of(t0, lp0, ph0);
-      fetch(cur, lp0, ph0);
-      ids_of(t0 + 1, lp1, ph1);
-    }
-    for (int k = 0; ok && k < nt; ++k) {
-      const int st = k % ST, t = t0 + k;
-      const bool blk = t >= ks.pt;
-      int lp2[CH], ph2[CH];
-      fetch(nxt, lp1, ph1);
-      ids_of(t + 2, lp2, ph2);
-      int elp = -1, ephys = -1;  // the table's entry of this lane
-      if (tid < PPT) page_at(t, tid, elp, ephys);
-      bool full = false;
-      int u0 = 0, u_end = 0;
-      if (blk) u0 = blk_tile(t, u_end, full);
-      if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(st), ((k / ST) - 1) & 1, ctx));
-      if (!ok) break;
-      const uint32_t bytes = (uint32_t)prm.box_blk * 128u * C::kHalves;
-      const uint32_t ok_k = C::kOffK + st * C::kTile, ok_v = C::kOffV + st * C::kTile;
-      if (blk) {
-        if (tid == 0) {
-          mbar_arrive_expect_tx(k_full(st), bytes);
-          for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(base + ok_k + hf * C::kHalf, &bkmap, k_full(st), hf * 64, h, s * sh.B + u0);
+    while (ok && walk.next()) {
+      const Keys &ks = walk.ks;
+      int lp = -1, phys = -1;
+      if (lane < PPT) walk.page_at(walk.t0, lane, lp, phys);
+      for (int j = 0; j < walk.nt; ++j, ++k) {
+        const int st = k % ST, t = walk.t0 + j;
+        int lp1 = -1, phys1 = -1;  // the next tile's pages, fetched before this tile's wait
+        if (j + 1 < walk.nt && lane < PPT) walk.page_at(t + 1, lane, lp1, phys1);
+        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
+        if (!ok) break;
+        if (!isv) {
+          walk.put_table(table(k), t, lane, lp, phys);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tab_full(k));
+        }
+        const uint32_t dst = ring + st * C::kTile;
+        if (t >= ks.pt) {
+          int u_end;
+          bool f;
+          const int u0 = walk.blk_tile(t, u_end, f);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full(st), (uint32_t)prm.box_blk * 128u * C::kHalves);
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d(dst + hf * C::kHalf, bmap, full(st), hf * 64, ks.h, ks.s * sh.B + u0);
+          } else {
+            mbar_arrive(full(st));
+          }
+        } else if (kBoxes) {
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, lane < PPT && phys >= 0)) * PAGE * 128u * C::kHalves;
+          if (lane == 0)
+            mbar_arrive_expect_tx(full(st), bytes);
+          else
+            mbar_arrive(full(st));
+          __syncwarp();
+          const int e = lane % PPT, hf = lane / PPT;
+          const int ph = __shfl_sync(0xffffffffu, phys, e);
+          if (hf < C::kHalves && ph >= 0)
+            tma_load_2d(dst + hf * C::kHalf + e * PAGE * 128u, map, full(st), hf * 64, (int)(((long long)ph * sh.Hkv + ks.h) * PAGE));
         } else {
-          mbar_arrive(k_full(st));
-        }
-      } else {
-        put(ok_k, cur.k, cur.ks, lp0, ph0);
-        fence_proxy_async_smem();
-        mbar_arrive(k_full(st));
-      }
-      if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(st), ((k / ST) - 1) & 1, ctx));
-      issued = k + 1;
-      if (!ok) break;
-      if (tid < 32) {
-        int *tab = table(st);
-        if (blk) {
-          if (tid == 0) tab[0] = ks.n + u0;
-        } else {
-          if (elp != -1 && ephys < 0) raise_status(a.status, kStatusBadIndex);
-          if (tid < PPT) tab[tid] = ephys >= 0 ? elp * PAGE : kNever;
-          full = __all_sync(0xffffffffu, tid >= PPT || page_full(elp, ephys));
-        }
-        if (tid == 0) {
-          tab[8] = (full ? 1 : 0) | (blk ? 2 : 0);
-          tab[9] = blk ? ks.n + u_end : ks.n;
-        }
-        __syncwarp();
-      }
-      if (blk) {
-        if (tid == 0) {
-          mbar_arrive_expect_tx(v_full(st), bytes);
-          for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(base + ok_v + hf * C::kHalf, &bvmap, v_full(st), hf * 64, h, s * sh.B + u0);
-        } else {
-          mbar_arrive(v_full(st));
-        }
-      } else {
-        put(ok_v, cur.v, cur.vs, lp0, ph0);
-        fence_proxy_async_smem();
-        mbar_arrive(v_full(st));
-      }
-      cur = nxt;
+          // 16 bytes a lane; D / 8 lanes hold a row
+          constexpr int LPR = D / 8;
+          const int cr = lane % LPR, row0 = lane / LPR;
+          const uint32_t dcol = (cr >> 3) * C::kHalf;
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        lp0[i] = lp1[i]; ph0[i] = ph1[i];
-        lp1[i] = lp2[i]; ph1[i] = ph2[i];
+          for (int e = 0; e < PPT; ++e) {
+            const int ph = __shfl_sync(0xffffffffu, phys, e);
+            if (ph < 0) continue;
+            const __nv_bfloat16 *src = cache + (((long long)ph * sh.Hkv + ks.h) * PAGE + row0) * D + cr * 8;
+#pragma unroll
+            for (int i = 0; i < PAGE / (32 / LPR); ++i) {
+              const int key = e * PAGE + i * (32 / LPR) + row0;
+              cp_async16(dst + dcol + sw128_offset(key, cr & 7), src + (long long)i * (32 / LPR) * D);
+            }
+          }
+        }
+        if (!kBoxes) {
+          cp_async_commit();
+          if (k > 0) {  // the tile before has landed: announce it (unless TMA does)
+            cp_async_wait<1>();
+            if (told < k) {
+              fence_proxy_async_smem();
+              mbar_arrive(full((k - 1) % ST));
+            }
+          }
+          told = t >= ks.pt ? k + 1 : k;  // tiles whose arrivals are made
+        }
+        lp = lp1;
+        phys = phys1;
       }
     }
-    if (tid == 0) {  // copies in flight land before the CTA's shared memory is released
-      for (int k = max(0, issued - ST); k < issued; ++k) {
-        if (t0 + k < ks.pt) continue;
-        mbar_wait(k_full(k % ST), (k / ST) & 1, drain_ctx);
-        if (ok) mbar_wait(v_full(k % ST), (k / ST) & 1, drain_ctx);
+    if (!kBoxes) {
+      cp_async_wait<0>();
+      if (told < k) {
+        fence_proxy_async_smem();
+        mbar_arrive(full((k - 1) % ST));
       }
     }
+    // copies in flight land before the CTA's shared memory is released
+    if (lane == 0)
+      for (int j = max(0, k - ST); j < k; ++j) mbar_wait(full(j % ST), (j / ST) & 1, drain_ctx);
+    __syncwarp();
+  } else {
+    // ------------------------------------------- 4-bit rows into bf16 tiles --
+    // 64 threads each for K and V.  Packed tiles come in by 16-byte asynchronous copies,
+    // two tiles ahead; a thread then turns 16 bytes (a group of 32 values) at a time into
+    // 64 bytes of a swizzled row.
+    const bool isv = warp >= 12;
+    const int tid = (threadIdx.x - 320) & 63;
+    constexpr int GR = D / kKv4Group;            // groups of a row
+    constexpr int CH = kBN * GR / 64;            // 16-byte chunks of a thread
+    constexpr int RPS = 16 / (2 * GR);           // rows whose scales are 16 bytes
+    const uint8_t *codes = isv ? a.kv4.v : a.kv4.k;
+    const __nv_bfloat16 *scales = isv ? a.kv4.vs : a.kv4.ks;
+    const CUtensorMap *bmap = isv ? &bvmap : &bkmap;
+    auto full = [&](int st) { return isv ? v_full(st) : k_full(st); };
+    auto empty = [&](int st) { return isv ? v_empty(st) : k_empty(st); };
+    const uint32_t ring = isv ? C::kOffV : C::kOffK;
+    const uint32_t rawring = C::kOffRaw + (isv ? C::kRawSlots * C::kRaw : 0);
+    int k = 0, gathered = 0;
+    bool ok = true;
+    auto gather = [&]() {  // the 64 threads; a bounded wait, unlike a named barrier
+      mbar_arrive(loaders(isv));
+      ok = __all_sync(0xffffffffu, mbar_wait(loaders(isv), gathered & 1, ctx));
+      ++gathered;
+      return ok;
+    };
+    while (ok && walk.next()) {
+      const Keys &ks = walk.ks;
+      // pages of the tiles j, j + 1, j + 2 of the piece: lane e holds page e
+      int lp[3], ph[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        lp[i] = ph[i] = -1;
+        if (i < walk.nt && lane < PPT) walk.page_at(walk.t0 + i, lane, lp[i], ph[i]);
+      }
+      auto load = [&](int slot, int phys) {
+        const uint32_t dst = base + rawring + slot * C::kRaw;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int c = tid + 64 * i, key = c / GR;
+          const int p = __shfl_sync(0xffffffffu, phys, key / PAGE);
+          if (p >= 0)
+            cp_async16(dst + c * 16, codes + (((long long)p * sh.Hkv + ks.h) * PAGE + key % PAGE) * (D / 2) + (c % GR) * 16);
+        }
+        const int key = tid * RPS;
+        const int p = __shfl_sync(0xffffffffu, phys, min(key, kBN - 1) / PAGE);
+        if (key < kBN && p >= 0)
+          cp_async16(dst + C::kRawCodes + tid * 16, scales + (((long long)p * sh.Hkv + ks.h) * PAGE + key % PAGE) * GR);
+        cp_async_commit();
+      };
+      if (!gather()) break;  // all of the 64 threads have read the piece before
+      load(k % 3, ph[0]);
+      load((k + 1) % 3, ph[1]);
+      for (int j = 0; j < walk.nt; ++j, ++k) {
+        const int st = k % ST, t = walk.t0 + j;
+        const bool blk = t >= ks.pt;
+        int lp3 = -1, ph3 = -1;
+        if (j + 3 < walk.nt && lane < PPT) walk.page_at(t + 3, lane, lp3, ph3);
+        cp_async_wait<1>();
+        if (!gather()) break;  // everybody's part of tile j is there, and tile j - 1 is read
+        load((k + 2) % 3, ph[2]);
+        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
+        if (!ok) break;
+        if (warp == 10) {
+          walk.put_table(table(k), t, lane, lp[0], ph[0]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tab_full(k));
+        }
+        if (blk) {
+          if (tid == 0) {
+            int u_end;
+            bool f;
+            const int u0 = walk.blk_tile(t, u_end, f);
+            mbar_arrive_expect_tx(full(st), (uint32_t)prm.box_blk * 128u * C::kHalves);
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d(base + ring + st * C::kTile + hf * C::kHalf, bmap, full(st), hf * 64, ks.h, ks.s * sh.B + u0);
+          } else {
+            mbar_arrive(full(st));
+          }
+        } else {
+          const unsigned char *src = smem + rawring + (k % 3) * C::kRaw;
+          unsigned char *dst = smem + ring + st * C::kTile;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int c = tid + 64 * i, key = c / GR, grp = c % GR;
+            const int p = __shfl_sync(0xffffffffu, ph[0], key / PAGE), q = __shfl_sync(0xffffffffu, lp[0], key / PAGE);
+            const bool on = p >= 0 && q * PAGE + key % PAGE < ks.n;
+            uint4 w = *reinterpret_cast<const uint4 *>(src + c * 16);
+            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + c * 2);
+            __nv_bfloat162 s8, m24;
+            kv4_constants(sc, s8, m24);
+            if (!on) {  // code 8 with scale 0 is the value 0
+              w = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+              s8 = m24 = __float2bfloat162_rn(0.f);
+            }
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              *reinterpret_cast<uint4 *>(dst + (grp / 2) * C::kHalf + sw128_offset(key, (grp % 2) * 4 + q4)) =
+                  make_uint4(kv4_pair(ww[q4], 0, s8, m24), kv4_pair(ww[q4], 1, s8, m24), kv4_pair(ww[q4], 2, s8, m24),
+                             kv4_pair(ww[q4], 3, s8, m24));
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(full(st));
+        }
+        lp[0] = lp[1]; ph[0] = ph[1];
+        lp[1] = lp[2]; ph[1] = ph[2];
+        lp[2] = lp3; ph[2] = ph3;
+      }
+      cp_async_wait<0>();
+    }
+    if (tid == 0)  // copies in flight land before the CTA's shared memory is released
+      for (int j = max(0, k - ST); j < k; ++j) mbar_wait(full(j % ST), (j / ST) & 1, drain_ctx);
+    __syncwarp();
   }
 
-  // ---- join the groups and write the rows (or their share, for the merge)
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();  // every MMA is done: Q, K and V are dead
-  tc_fence_after();
-  float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffML);
-  if (warp >= 2 && warp < 10) ml[((warp - 2) >> 2) * 128 + (warp & 3) * 32 + lane] = make_float2(m_used, l);
-  __syncthreads();
-  if (warp >= 2 && warp < 10 && (warp & 3) < active_warps) {
-    const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lt = tmem + ((uint32_t)(quarter * 32) << 16) + C::kTmemO;
-    const float2 x = ml[r], y = ml[128 + r];
-    const bool hx = x.y != 0.f, hy = y.y != 0.f;  // a NaN sum counts as data
-    const float M = fmaxf(hx ? x.x : -INFINITY, hy ? y.x : -INFINITY);
-    const float M0 = M == -INFINITY ? 0.f : M;
-    float wx = hx ? exp2f(x.x == -INFINITY ? 0.f : x.x - M0) : 0.f, wy = hy ? exp2f(y.x == -INFINITY ? 0.f : y.x - M0) : 0.f;
-    const float L = (hx ? wx * x.y : 0.f) + (hy ? wy * y.y : 0.f);
-    const bool warp_x = __any_sync(0xffffffffu, hx), warp_y = __any_sync(0xffffffffu, hy);
-    const bool mine = r < rows;
-    const size_t orow = ((size_t)s * sh.B + b0 + r / sh.G) * sh.Hq + (size_t)h * sh.G + r % sh.G;
-    const size_t prow = ((size_t)unit * prm.splits + sp) * ((size_t)prm.bpt * sh.G) + r;
-    const bool direct = prm.splits == 1;
-    const float inv = L != 0.f ? 1.f / L : 0.f;
-    if (mine && g == 0) {
-      if (!direct) prm.part_ml[prow] = make_float2(M, L);
-      if (direct && sh.lse_out)
-        sh.lse_out[orow] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-    }
-    if (direct) {
-      wx *= inv;
-      wy *= inv;
-    }
-    for (int c0 = g * (D / 2); c0 < (g + 1) * (D / 2); c0 += 32) {  // each group half of the columns
-      uint32_t u[32], v[32];
-      if (warp_x && warp_y) {
-        tmem_ld32x2(lt + c0, u, lt + D + c0, v);
-      } else {
-        if (warp_x) tmem_ld32(lt + c0, u);
-        if (warp_y) tmem_ld32(lt + D + c0, v);
-      }
-      float o[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i)  // an accumulator without data is never touched
-        o[i] = (hx ? wx * __uint_as_float(u[i]) : 0.f) + (hy ? wy * __uint_as_float(v[i]) : 0.f);
-      if (mine && direct) {
-        uint4 *dst = reinterpret_cast<uint4 *>(a.o_out + orow * D + c0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                              pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-      } else if (mine && L != 0.f) {
-        float4 *dst = reinterpret_cast<float4 *>(prm.part_o + prow * D + c0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
-      __syncwarp();  // the TMEM loads are warp-collective
-    }
-  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -709,36 +917,45 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   }
 }
 
-// Joins the splits of each row: one warp per row, D/32 columns a lane.
-constexpr int kMergeThreads = 128;
+// Joins the pieces of the units that shares cut: block x = c - 1 takes the unit that CTA
+// c - 1 began and left (its later pieces are the first ones of CTAs c, c + 1, ...); a warp
+// per row, D/32 columns a lane.  The pieces are joined in their order.
+constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_constant__ Params prm) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   const Shape &sh = prm.sh;
-  const int lane = threadIdx.x & 31;
   const int rpt = prm.bpt * sh.G;  // rows of a unit
-  const long long w = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  const int unit = (int)(w / rpt), r = (int)(w % rpt);
-  const int rt = unit % prm.rowtiles, h = unit / prm.rowtiles % sh.Hkv, s = unit / prm.rowtiles / sh.Hkv;
-  if (s >= sh.S) return;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const Piece p = prm.piece[2 * blockIdx.x + 1];
+  if (p.unit < 0 || r >= rpt) return;
+  const int rt = p.unit % prm.rowtiles, h = p.unit / prm.rowtiles % sh.Hkv, s = p.unit / prm.rowtiles / sh.Hkv;
   const int b = rt * prm.bpt + r / sh.G;
   if (b >= block_tokens(prm.a.n_new, s, sh.B, prm.a.status, false)) return;
   constexpr int E = D / 32;
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int sp = 0; sp < prm.splits; ++sp) {
-    const size_t prow = ((size_t)unit * prm.splits + sp) * rpt + r;
+  int slot = 2 * blockIdx.x + 1;
+  for (int c = blockIdx.x; c <= (int)gridDim.x; ++c) {  // CTAs 0 .. gridDim.x
+    const size_t prow = (size_t)slot * rpt + r;
     const float2 ml = prm.part_ml[prow];
-    if (ml.y == 0.f) continue;  // no key, nothing written
-    const float mn = fmaxf(M, ml.x);
-    const float sc = M == -INFINITY ? 0.f : exp2f(M - mn), wt = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mn);
-    M = mn;
-    L = fmaf(L, sc, wt * ml.y);
-    const float *src = prm.part_o + prow * D + lane * E;
+    const bool ends = prm.piece[slot].ends;
+    float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], sc, wt * src[e]);
+    for (int e = 0; e < E; ++e) v[e] = prm.part_o[prow * D + lane * E + e];
+    if (ml.y != 0.f) {  // a piece without a visible key holds zeros
+      const float mn = fmaxf(M, ml.x);
+      const float sc = M == -INFINITY ? 0.f : exp2f(M - mn), wt = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mn);
+      M = mn;
+      L = fmaf(L, sc, wt * ml.y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], sc, wt * v[e]);
+    }
+    if (ends) break;
+    slot = 2 * (c + 1);
   }
   const size_t orow = ((size_t)s * sh.B + b) * sh.Hq + (size_t)h * sh.G + r % sh.G;
   const float inv = L != 0.f ? 1.f / L : 0.f;
@@ -761,26 +978,15 @@ Geometry geometry(const Shape &sh) {
   return g;
 }
 
-// Splits: the count whose waves of CTAs (one per SM) take the least time, a CTA
-// costing its tiles plus a fixed part (set-up and epilogue), a split row the merge.
-// The workspace holds the largest count a shape may get, whatever its window.
-int max_splits(const Geometry &g, int sms) { return (int)std::max(1LL, std::min(64LL, 4LL * sms / g.units)); }
 PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles) {
   const Geometry g = geometry(sh);
-  const int cap = max_splits(g, sms);
-  PagedPlan p{1, 1, 0};
-  long long best = -1;
-  for (int sp = 1; sp <= cap && sp <= max_tiles; ++sp) {
-    const long long waves = (g.units * sp + sms - 1) / sms;
-    const long long cost = waves * ((max_tiles + sp - 1) / sp + 3) + (sp > 1 ? 2 : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.splits = sp;
-    }
-  }
-  p.launches = p.splits > 1 ? 2 : 1;
-  p.total = kWorkspaceHeader;
-  if (cap > 1) p.total += (size_t)g.units * cap * g.rows * ((size_t)sh.d * 4 + 8);
+  PagedPlan p{};
+  // whole units where there are many, or where none is long enough to be cut
+  p.shared_out = g.units <= (long long)kManyUnits * sms && g.units <= kUnitsPerThread * 384 && max_tiles > kMinTiles;
+  p.ctas = p.shared_out ? sms : (int)std::min<long long>(sms, g.units);
+  p.launches = p.shared_out && sms > 1 ? 2 : 1;
+  // the same for every window, so that one workspace serves a model's layers
+  p.total = kWorkspaceHeader + 2 * (size_t)sms * (sizeof(Piece) + g.rows * ((size_t)sh.d * 4 + 8));
   return p;
 }
 
@@ -788,40 +994,40 @@ template <int D, int PAGE, bool KV4>
 cudaError_t launch_typed(const Shape &sh, const PagedPlan &plan, const PagedArgs &a, cudaStream_t stream) {
   using C = Cfg<D, KV4>;
   const Geometry g = geometry(sh);
-  if (g.units * plan.splits > INT_MAX) return cudaErrorInvalidValue;
+  if (g.units > INT_MAX) return cudaErrorInvalidValue;
   Params prm{};
   prm.sh = sh;
   prm.a = a;
   prm.bpt = g.bpt;
   prm.rowtiles = g.rowtiles;
-  prm.splits = plan.splits;
+  prm.units = (int)g.units;
+  prm.shared_out = plan.shared_out;
   prm.box_blk = std::min(kBN, (sh.B + 15) / 16 * 16);
   unsigned char *ws = reinterpret_cast<unsigned char *>(a.status) + kWorkspaceHeader;
-  const size_t rows = (size_t)g.units * plan.splits * g.rows;
-  prm.part_o = reinterpret_cast<float *>(ws);
-  prm.part_ml = reinterpret_cast<float2 *>(ws + rows * D * 4);
+  const size_t slots = 2 * (size_t)plan.ctas;
+  prm.piece = reinterpret_cast<Piece *>(ws);
+  prm.part_o = reinterpret_cast<float *>(ws + slots * sizeof(Piece));
+  prm.part_ml = reinterpret_cast<float2 *>(prm.part_o + slots * g.rows * D);
   constexpr auto kern = paged_attn<D, PAGE, KV4>;
   cudaError_t err = set_smem_once<kern>(C::kAlloc);
   if (err != cudaSuccess) return err;
-  CUtensorMap q{}, k{}, v{}, k4{}, v4{}, bk{}, bv{};
+  CUtensorMap q{}, k{}, v{}, bk{}, bv{};
   const long long tokens = (long long)sh.S * sh.B;
   if ((err = make_q_tensor_map(&q, a.q, tokens, sh.Hq, D, sh.G, g.bpt)) != cudaSuccess) return err;
-  if (!KV4) {
+  if (!KV4 && PAGE >= 64) {
     const long long nrows = sh.n_phys * sh.Hkv * PAGE;
     if ((err = make_kv_tensor_map(&k, a.k, nrows, D, PAGE)) != cudaSuccess) return err;
     if ((err = make_kv_tensor_map(&v, a.v, nrows, D, PAGE)) != cudaSuccess) return err;
-    if ((err = make_kv_pages_tensor_map(&k4, a.k, sh.n_phys, sh.Hkv, PAGE, D, kBN / PAGE)) != cudaSuccess) return err;
-    if ((err = make_kv_pages_tensor_map(&v4, a.v, sh.n_phys, sh.Hkv, PAGE, D, kBN / PAGE)) != cudaSuccess) return err;
   }
   if (a.blk_k) {
     if ((err = make_blk_tensor_map(&bk, a.blk_k, tokens, sh.Hkv, D, prm.box_blk)) != cudaSuccess) return err;
     if ((err = make_blk_tensor_map(&bv, a.blk_v, tokens, sh.Hkv, D, prm.box_blk)) != cudaSuccess) return err;
   }
-  err = launch_pdl(kern, dim3((unsigned)(g.units * plan.splits)), C::kThreads, C::kAlloc, stream, prm, q, k, v, k4, v4, bk, bv);
-  if (err != cudaSuccess || plan.splits == 1) return err;
-  const long long merge_rows = g.units * g.rows;
-  return launch_pdl(paged_merge<D>, dim3((unsigned)((merge_rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32))),
-                    kMergeThreads, 0, stream, prm);
+  err = launch_pdl(kern, dim3((unsigned)plan.ctas), C::kThreads, C::kAlloc, stream, prm, q, k, v, bk, bv);
+  if (err != cudaSuccess || plan.launches == 1) return err;
+  constexpr int kWarps = kMergeThreads / 32;
+  return launch_pdl(paged_merge<D>, dim3((unsigned)(plan.ctas - 1), (unsigned)((g.rows + kWarps - 1) / kWarps)), kMergeThreads, 0,
+                    stream, prm);
 }
 
 template <bool KV4>
