@@ -174,6 +174,7 @@ struct PagedArgs {
   uint32_t *status;
 };
 struct PagedPlan {
+  int few;        // 1: at most 16 rows per (sequence, KV head): the kernel for few rows
   int ctas;
   int shared_out; // 1: the units' tiles are cut into equal shares, 0: CTAs take whole units
   int launches;

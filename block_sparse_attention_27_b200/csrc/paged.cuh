@@ -44,6 +44,10 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int i, __nv_bfloat162 s
   __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&y), s8, m24);
   return *reinterpret_cast<uint32_t *>(&r);
 }
+__device__ __forceinline__ void kv4_constants(__nv_bfloat162 s, __nv_bfloat162 &s8, __nv_bfloat162 &m24) {
+  s8 = __hmul2(s, __float2bfloat162_rn(0.125f));
+  m24 = __hmul2(s, __float2bfloat162_rn(-24.f));
+}
 __device__ __forceinline__ void kv4_constants(__nv_bfloat16 s, __nv_bfloat162 &s8, __nv_bfloat162 &m24) {
   const float f = __bfloat162float(s);
   s8 = __float2bfloat162_rn(f * 0.125f);

@@ -29,6 +29,7 @@
 // 2^8, so O is rarely rescaled.  Sums, maxima and outputs are held in fp32, P alone in
 // bf16: one MMA takes both operands in one type, and V is bf16.
 #include <climits>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -44,7 +45,7 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr int kTabs = 8;        // tiles whose positions are kept: six are in flight at most
 constexpr int kMinTiles = 2;    // least tiles of a share
 constexpr int kManyUnits = 8;   // units per CTA from which shares are whole units
-constexpr int kUnitsPerThread = 4;  // of the scan over the units' tiles: 8 * 148 <= 4 * 320
+constexpr int kMaxShared = 1536;  // most units that are cut into equal shares
 
 template <int D, bool KV4>
 struct Cfg {
@@ -275,6 +276,62 @@ struct Walk {
   }
 };
 
+// This CTA's share, by a scan over the units' tiles: share[0..2] = its first unit, the
+// first tile of it, its number of tiles.  All threads; ends with a CTA barrier.  `sums`: an
+// int per warp.
+template <bool KV4, int PAGE, int THREADS>
+__device__ __forceinline__ void cta_share(const Params &prm, int *share, int *sums) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    share[0] = prm.shared_out ? prm.units : (int)blockIdx.x;
+    share[1] = 0;
+    share[2] = prm.shared_out ? 0 : INT_MAX;
+  }
+  if (prm.shared_out) {
+    constexpr int kUnits = (kMaxShared + THREADS - 1) / THREADS;  // of a thread
+    const int u0 = threadIdx.x * kUnits;
+    int cnt[kUnits], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      cnt[i] = 0;
+      if (u0 + i < prm.units) {
+        Limits x, y;
+        cnt[i] = unit_keys<KV4, PAGE>(prm, u0 + i, x, y, blockIdx.x == 0).tiles;
+      }
+      mine += cnt[i];
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      before += w < warp ? sums[w] : 0;
+      total += sums[w];
+    }
+    const int shares = max(1, min((int)gridDim.x, total / kMinTiles));
+    const int c = blockIdx.x;
+    if (c < shares) {
+      const int lo = (int)((long long)total * c / shares), hi = (int)((long long)total * (c + 1) / shares);
+      int at = before + upto - mine;  // first tile of this thread's units
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        if (lo >= at && lo < at + cnt[i]) {
+          share[0] = u0 + i;
+          share[1] = lo - at;
+          share[2] = hi - lo;
+        }
+        at += cnt[i];
+      }
+    }
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -350,8 +407,6 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     mbar_init(loaders(true), 64);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    scan[0] = prm.units;
-    scan[1] = scan[2] = 0;
     fence_mbar_init();
     tma_prefetch_map(&qmap);
   }
@@ -362,52 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  // ---- this CTA's share: a scan over the units' tiles
-  if (prm.shared_out) {
-    int *sums = reinterpret_cast<int *>(m_ref);  // of the warps
-    const int u0 = threadIdx.x * kUnitsPerThread;
-    int cnt[kUnitsPerThread], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kUnitsPerThread; ++i) {
-      cnt[i] = 0;
-      if (u0 + i < prm.units) {
-        Limits x, y;
-        cnt[i] = unit_keys<KV4, PAGE>(prm, u0 + i, x, y, blockIdx.x == 0).tiles;
-      }
-      mine += cnt[i];
-    }
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      before += w < warp ? sums[w] : 0;
-      total += sums[w];
-    }
-    const int shares = max(1, min((int)gridDim.x, total / kMinTiles));
-    const int c = blockIdx.x;
-    if (c < shares) {
-      const int lo = (int)((long long)total * c / shares), hi = (int)((long long)total * (c + 1) / shares);
-      int at = before + upto - mine;  // first tile of this thread's units
-#pragma unroll
-      for (int i = 0; i < kUnitsPerThread; ++i) {
-        if (lo >= at && lo < at + cnt[i]) {
-          scan[0] = u0 + i;
-          scan[1] = lo - at;
-          scan[2] = hi - lo;
-        }
-        at += cnt[i];
-      }
-    }
-  } else if (threadIdx.x == 0) {
-    scan[0] = blockIdx.x;
-    scan[2] = INT_MAX;
-  }
+  cta_share<KV4, PAGE, C::kThreads>(prm, scan, reinterpret_cast<int *>(m_ref));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -917,6 +927,471 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------- few rows ----
+// Units of at most 16 query rows (decoding) are bound by the cache's bytes: a 128-row MMA
+// would idle on them.  Here a warp takes 16 keys of each tile straight from global
+// memory into the fragments of mma.m16n8k16, with no shared memory between:
+//   S^T = K Q^T  (16 keys x 8 rows; the order of the contraction over d is free, so a
+//                 lane's K fragments are 16 contiguous bytes)
+//   O^T += V^T P^T  (d x 8 rows; the order of d over the M rows is free, so a lane's V
+//                 fragments are D/8 contiguous values of four keys, pairs of keys
+//                 interleaved by byte permutes, while still packed in the 4-bit cache)
+// P goes from the accumulators' layout to the operand's by a transposing 8x8 move.  P is
+// taken as the sum of two bf16 numbers (17 bits): the second product is free here.
+// A lane owns the maxima and sums of the rows 2t, 2t + 1 of its column.
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 16;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_stream(const uint2 *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_stream(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// 16 keys on their way into fragments.
+template <int D>
+struct KeysBf16 {
+  uint32_t k[2][D / 8], v[4][D / 16];
+  // K of keys g, g + 8: chunks t, t + 4, .. of 16 bytes; V of keys 2t, 2t+1, 2t+8, 2t+9: D/8 values
+  __device__ __forceinline__ void load_k(const __nv_bfloat16 *row, long long stride, int g, int t, uint32_t on) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if ((on >> (g + 8 * i)) & 1u) x = ld_stream(reinterpret_cast<const uint4 *>(row + (g + 8 * i) * stride) + t + 4 * c);
+        k[i][4 * c] = x.x; k[i][4 * c + 1] = x.y; k[i][4 * c + 2] = x.z; k[i][4 * c + 3] = x.w;
+      }
+  }
+  __device__ __forceinline__ void load_v(const __nv_bfloat16 *row, long long stride, int g, int t, uint32_t on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * t + (i & 1) + 4 * (i & 2);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if ((on >> key) & 1u) x = ld_stream(reinterpret_cast<const uint4 *>(row + key * stride + (D / 8) * g) + c);
+        v[i][4 * c] = x.x; v[i][4 * c + 1] = x.y; v[i][4 * c + 2] = x.z; v[i][4 * c + 3] = x.w;
+      }
+    }
+  }
+  // first element of the four of a lane in step j of the contraction
+  static __device__ __forceinline__ int k_at(int t, int j) { return (t + 4 * (j >> 1)) * 8 + 4 * (j & 1); }
+  __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) const {
+    a[0] = k[0][2 * j]; a[1] = k[1][2 * j]; a[2] = k[0][2 * j + 1]; a[3] = k[1][2 * j + 1];
+  }
+  __device__ __forceinline__ void v_frag(int i, uint32_t (&a)[4]) const {
+    a[0] = __byte_perm(v[0][i], v[1][i], 0x5410);
+    a[1] = __byte_perm(v[0][i], v[1][i], 0x7632);
+    a[2] = __byte_perm(v[2][i], v[3][i], 0x5410);
+    a[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+  }
+};
+template <int D>
+struct KeysKv4 {
+  static constexpr int KWords = D / 32, VWords = D / 64;  // packed words of a lane per key
+  uint32_t k[2][KWords], v[4][VWords];
+  uint16_t sk[2], sv[4];
+  __device__ __forceinline__ void load_k(const uint8_t *row, const __nv_bfloat16 *sc, int g, int t, uint32_t on) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = g + 8 * i;
+      const bool o = (on >> key) & 1u;
+      sk[i] = 0;
+#pragma unroll
+      for (int w = 0; w < KWords; ++w) k[i][w] = 0x88888888u;
+      if (!o) continue;
+      if constexpr (D == 128) {
+        const uint4 x = ld_stream(reinterpret_cast<const uint4 *>(row + key * (D / 2)) + t);
+        k[i][0] = x.x; k[i][1] = x.y; k[i][2] = x.z; k[i][3] = x.w;
+      } else {
+        const uint2 x = ld_stream(reinterpret_cast<const uint2 *>(row + key * (D / 2)) + t);
+        k[i][0] = x.x; k[i][1] = x.y;
+      }
+      sk[i] = __ldg(reinterpret_cast<const uint16_t *>(sc) + key * (D / kKv4Group) + t * (D / 4) / kKv4Group);
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint8_t *row, const __nv_bfloat16 *sc, int g, int t, uint32_t on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * t + (i & 1) + 4 * (i & 2);
+      sv[i] = 0;
+#pragma unroll
+      for (int w = 0; w < VWords; ++w) v[i][w] = 0x88888888u;
+      if (!((on >> key) & 1u)) continue;
+      if constexpr (D == 128) {
+        const uint2 x = ld_stream(reinterpret_cast<const uint2 *>(row + key * (D / 2)) + g);
+        v[i][0] = x.x; v[i][1] = x.y;
+      } else {
+        v[i][0] = ld_stream(reinterpret_cast<const uint32_t *>(row + key * (D / 2)) + g);
+      }
+      sv[i] = __ldg(reinterpret_cast<const uint16_t *>(sc) + key * (D / kKv4Group) + g * (D / 8) / kKv4Group);
+    }
+  }
+  static __device__ __forceinline__ int k_at(int t, int j) { return (D / 4) * t + 4 * j; }
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint16_t a, uint16_t b) {
+    const uint32_t x = (uint32_t)a | ((uint32_t)b << 16);
+    return *reinterpret_cast<const __nv_bfloat162 *>(&x);
+  }
+  __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      __nv_bfloat162 s8, m24;
+      kv4_constants(pair(sk[i], sk[i]), s8, m24);
+      a[i] = kv4_pair(k[i][j >> 1], 2 * (j & 1), s8, m24);
+      a[i + 2] = kv4_pair(k[i][j >> 1], 2 * (j & 1) + 1, s8, m24);
+    }
+  }
+  __device__ __forceinline__ void v_frag(int i, uint32_t (&a)[4]) const {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      __nv_bfloat162 s8, m24;
+      kv4_constants(pair(sv[2 * p], sv[2 * p + 1]), s8, m24);
+      const uint32_t x = v[2 * p][i >> 2], y = v[2 * p + 1][i >> 2];
+      a[2 * p] = kv4_pair(__byte_perm(x, y, 0x5410), i & 3, s8, m24);
+      a[2 * p + 1] = kv4_pair(__byte_perm(x, y, 0x7632), i & 3, s8, m24);
+    }
+  }
+};
+
+// O^T and the statistics of a warp's keys, for 8 * NT rows.
+template <int D, int NT>
+struct FewState {
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];  // rows 8 n + 2t, 8 n + 2t + 1; l of this lane's keys
+};
+
+// One step: 16 keys of fragments `f`; `hid` bit 4 n + 2 i + e: key g + 8 i is hidden from row 8 n + 2t + e.
+template <int D, int NT, class F>
+__device__ __forceinline__ void few_scores(const F &f, const uint2 *qf, int lane, float (&x)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    uint32_t a[4];
+    f.k_frag(j, a);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint2 b = qf[(n * (D / 16) + j) * 32 + lane];
+      mma_bf16(x[n], a[0], a[1], a[2], a[3], b.x, b.y);
+    }
+  }
+}
+template <int D, int NT>
+__device__ __forceinline__ void few_softmax(FewState<D, NT> &st, float (&x)[NT][4], uint32_t hid, float sl2,
+                                            uint32_t (&ph)[NT][2], uint32_t (&pl)[NT][2]) {
+  bool need = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[n][e] = (hid >> (4 * n + e)) & 1u ? -INFINITY : x[n][e] * sl2;
+      need |= x[n][e] > st.m[n][e & 1] + kRescaleLog2 || (st.m[n][e & 1] == -INFINITY && x[n][e] > -INFINITY);
+    }
+  if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = fmaxf(x[n][e], x[n][e + 2]);
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        const float mn = fmaxf(st.m[n][e], t);
+        const float al = st.m[n][e] == -INFINITY ? 0.f : st.m[n][e] == mn ? 1.f : fast_exp2(st.m[n][e] - mn);
+        st.m[n][e] = mn;
+        st.l[n][e] *= al;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          st.o[n][i][e] *= al;
+          st.o[n][i][e + 2] *= al;
+        }
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float p[4], q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float mu = st.m[n][e & 1] == -INFINITY ? 0.f : st.m[n][e & 1];
+      p[e] = fast_exp2(x[n][e] - mu);
+      st.l[n][e & 1] += p[e];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ph[n][i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+      const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ph[n][i]));
+      q[2 * i] = p[2 * i] - hi.x;
+      q[2 * i + 1] = p[2 * i + 1] - hi.y;
+      pl[n][i] = transpose8(pack_bf16x2(q[2 * i], q[2 * i + 1]));
+      ph[n][i] = transpose8(ph[n][i]);
+    }
+  }
+}
+template <int D, int NT, class F>
+__device__ __forceinline__ void few_values(const F &f, FewState<D, NT> &st, const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2]) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t a[4];
+    f.v_frag(i, a);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma_bf16(st.o[n][i], a[0], a[1], a[2], a[3], ph[n][0], ph[n][1]);
+      mma_bf16(st.o[n][i], a[0], a[1], a[2], a[3], pl[n][0], pl[n][1]);
+    }
+  }
+}
+
+template <int D, int NT>
+struct FewSmem {
+  static constexpr uint32_t kQ = 0;                                   // fragments [NT][D/16][32] x 8 bytes
+  static constexpr uint32_t kML = kQ + NT * (D / 16) * 32 * 8;         // [8 warps][8 NT rows] (m, l)
+  static constexpr uint32_t kO = kML + 8 * 8 * NT * 8;                 // [8 warps][8 NT rows][D + 4]
+  static constexpr int kRow = D + 4;                                   // spreads the rows over the banks
+  static constexpr uint32_t kBytes = kO + 8 * 8 * NT * kRow * 4;
+};
+
+template <int D, int PAGE, bool KV4, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 || KV4 ? 2 : 1) paged_few(const __grid_constant__ Params prm) {
+  using M = FewSmem<D, NT>;
+  extern __shared__ unsigned char smem_raw[];
+  uint2 *qf = reinterpret_cast<uint2 *>(smem_raw + M::kQ);
+  float2 *ml = reinterpret_cast<float2 *>(smem_raw + M::kML);
+  float *ow = reinterpret_cast<float *>(smem_raw + M::kO);
+  __shared__ int scan[3], sums[kFewThreads / 32];
+  const Shape &sh = prm.sh;
+  const PagedArgs &a = prm.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  cta_share<KV4, PAGE, kFewThreads>(prm, scan, sums);
+  Walk<KV4, PAGE> walk(prm, scan[0], scan[1], scan[2]);
+  if (threadIdx.x == 0 && prm.shared_out) prm.piece[2 * blockIdx.x].unit = prm.piece[2 * blockIdx.x + 1].unit = -1;
+  const int sub = warp;  // this warp's 16 keys of each tile
+  while (walk.next(!prm.shared_out && threadIdx.x == 0)) {
+    const Keys &ks = walk.ks;
+    // queries in the order of the contraction
+    for (int e = threadIdx.x; e < NT * (D / 16) * 32; e += kFewThreads) {
+      const int ln = e & 31, j = e / 32 % (D / 16), r = 8 * (e / 32 / (D / 16)) + (ln >> 2);
+      uint2 q = make_uint2(0, 0);
+      const int at = KV4 ? KeysKv4<D>::k_at(ln & 3, j) : KeysBf16<D>::k_at(ln & 3, j);
+      if (r < ks.rows)
+        q = *reinterpret_cast<const uint2 *>(a.q + (((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G) * D + at);
+      qf[e] = q;
+    }
+    __syncthreads();
+    Limits lim[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[n][e] = row_limits<KV4>(a, ks.n, ks.b0 + (8 * n + 2 * t4 + e) / sh.G);
+    const Limits all{walk.first.lb, walk.last.hi, walk.last.sk};
+    FewState<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        st.m[n][e] = -INFINITY;
+        st.l[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][i][e] = 0.f;
+    }
+    // which keys of the 16 at position `pos` (none at kNever) any row sees; bits of `hid` as above
+    auto masks = [&](int pos, int end, uint32_t &on, uint32_t &hid) {
+      on = visible(pos, 16, end, all);
+      hid = 0;
+      const bool full = pos != kNever && pos + 16 <= end &&
+                        (KV4 || pos + 16 <= walk.first.sk || (pos >= walk.last.lb && pos + 15 <= walk.first.hi));
+      if (full) return;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = visible(pos, 16, end, lim[n][e]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!((v >> (g + 8 * i)) & 1u)) hid |= 1u << (4 * n + 2 * i + e);
+        }
+    };
+    // ---- tiles of pages: page ids of 32 tiles at a time, a lane each
+    using F = typename std::conditional<KV4, KeysKv4<D>, KeysBf16<D>>::type;
+    constexpr int kDeep = KV4 ? 2 : 1;  // steps in flight ahead of the one being worked on
+    const int np = max(0, min(walk.nt, ks.pt - walk.t0));
+    F f[kDeep];
+    uint32_t on[kDeep], hid[kDeep];
+    int lps = -1, phs = -1;
+    auto row_of = [&](int j, int &pos) {  // row of the first of the warp's 16 keys in tile j of the piece
+      if ((j & 31) == 0) {
+        lps = phs = -1;
+        if (j + lane < np) walk.page_at(walk.t0 + j + lane, 16 * sub / PAGE, lps, phs);
+        if (lps != -1 && phs < 0 && (16 * sub) % PAGE == 0) raise_status(a.status, kStatusBadIndex);
+      }
+      const int lp = __shfl_sync(0xffffffffu, lps, j & 31), ph = __shfl_sync(0xffffffffu, phs, j & 31);
+      pos = ph >= 0 ? lp * PAGE + 16 * sub % PAGE : kNever;
+      return ((long long)max(ph, 0) * sh.Hkv + ks.h) * PAGE + 16 * sub % PAGE;
+    };
+    long long row[kDeep];
+    auto issue_k = [&](int d, int j) {
+      int pos;
+      row[d] = row_of(j, pos);
+      masks(pos, ks.n, on[d], hid[d]);
+      if constexpr (KV4)
+        f[d].load_k(a.kv4.k + row[d] * (D / 2), a.kv4.ks + row[d] * (D / kKv4Group), g, t4, on[d]);
+      else
+        f[d].load_k(a.k + row[d] * D, D, g, t4, on[d]);
+    };
+    auto issue_v = [&](int d) {
+      if constexpr (KV4)
+        f[d].load_v(a.kv4.v + row[d] * (D / 2), a.kv4.vs + row[d] * (D / kKv4Group), g, t4, on[d]);
+      else
+        f[d].load_v(a.v + row[d] * D, D, g, t4, on[d]);
+    };
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+      if (d < np) {
+        issue_k(d, d);
+        issue_v(d);
+      }
+    for (int j0 = 0; j0 < np; j0 += kDeep) {
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        if (j0 + d >= np) break;
+        float x[NT][4];
+        uint32_t ph[NT][2], pl[NT][2];
+        const bool some = on[d] != 0;  // the same in every lane
+        const uint32_t h = hid[d];
+        if (some) few_scores<D, NT>(f[d], qf, lane, x);
+        // K of the next step is on its way while this step's values are worked on, its V
+        // during the next scores
+        const bool more = j0 + d + kDeep < np;
+        if (more) issue_k(d, j0 + d + kDeep);
+        if (some) {
+          few_softmax<D, NT>(st, x, h, sh.sl2, ph, pl);
+          few_values<D, NT>(f[d], st, ph, pl);
+        }
+        if (more) issue_v(d);
+      }
+    }
+    // ---- tiles of block tokens (bf16)
+    for (int j = np; j < walk.nt; ++j) {
+      int u_end;
+      bool fl;
+      const int u = walk.blk_tile(walk.t0 + j, u_end, fl) + 16 * sub;
+      if (u >= u_end) continue;
+      uint32_t on0, hid0, ph[NT][2], pl[NT][2];
+      masks(ks.n + u, ks.n + u_end, on0, hid0);
+      if (!on0) continue;
+      KeysBf16<D> b;
+      const long long r0 = ((long long)ks.s * sh.B + u) * sh.Hkv + ks.h, stride = (long long)sh.Hkv * D;
+      b.load_k(a.blk_k + r0 * D, stride, g, t4, on0);
+      b.load_v(a.blk_v + r0 * D, stride, g, t4, on0);
+      float x[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+      for (int jj = 0; jj < D / 16; ++jj) {
+        uint32_t fr[4];
+        b.k_frag(jj, fr);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint2 q;
+          if constexpr (KV4) {  // the stored queries follow the packed order: fetch these from memory
+            const int r = 8 * n + g;
+            q = make_uint2(0, 0);
+            if (r < ks.rows)
+              q = *reinterpret_cast<const uint2 *>(a.q + (((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G) * D + KeysBf16<D>::k_at(t4, jj));
+          } else {
+            q = qf[(n * (D / 16) + jj) * 32 + lane];
+          }
+          mma_bf16(x[n], fr[0], fr[1], fr[2], fr[3], q.x, q.y);
+        }
+      }
+      few_softmax<D, NT>(st, x, hid0, sh.sl2, ph, pl);
+      few_values<D, NT>(b, st, ph, pl);
+    }
+    // ---- join the warps: sums over the lanes' keys, then (m, l, O) of each warp
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float &l = st.l[n][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int r = 8 * n + 2 * t4 + e;
+        if (g == 0) ml[warp * 8 * NT + r] = make_float2(st.m[n][e], l);
+        float *dst = ow + (warp * 8 * NT + r) * M::kRow + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          dst[2 * i] = st.o[n][i][e];
+          dst[2 * i + 1] = st.o[n][i][e + 2];
+        }
+      }
+    __syncthreads();
+    const bool whole = walk.begins() && walk.ends();
+    const int slot = 2 * blockIdx.x + (walk.begins() ? 1 : 0);
+    if (!whole && threadIdx.x == 0) prm.piece[slot] = Piece{walk.unit, walk.begins(), walk.ends(), 0};
+    for (int e = threadIdx.x; e < ks.rows * (D / 4); e += kFewThreads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float mx = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 v = ml[w * 8 * NT + r];
+        if (v.y != 0.f) mx = fmaxf(mx, v.x);
+      }
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 v = ml[w * 8 * NT + r];
+        if (v.y == 0.f) continue;
+        const float wt = v.x == -INFINITY ? 1.f : exp2f(v.x - mx);
+        L = fmaf(wt, v.y, L);
+        const float4 z = *reinterpret_cast<const float4 *>(ow + (w * 8 * NT + r) * M::kRow + c);
+        y.x = fmaf(wt, z.x, y.x); y.y = fmaf(wt, z.y, y.y); y.z = fmaf(wt, z.z, y.z); y.w = fmaf(wt, z.w, y.w);
+      }
+      const size_t orow = ((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G;
+      const size_t prow = (size_t)slot * ((size_t)prm.bpt * sh.G) + r;
+      if (whole) {
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint2 *>(a.o_out + orow * D + c) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+        if (c == 0 && sh.lse_out) sh.lse_out[orow] = L != 0.f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4 *>(prm.part_o + prow * D + c) = y;
+        if (c == 0) prm.part_ml[prow] = make_float2(mx, L);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // Joins the pieces of the units that shares cut: block x = c - 1 takes the unit that CTA
 // c - 1 began and left (its later pieces are the first ones of CTAs c, c + 1, ...); a warp
 // per row, D/32 columns a lane.  The pieces are joined in their order.
@@ -981,13 +1456,24 @@ Geometry geometry(const Shape &sh) {
 PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles) {
   const Geometry g = geometry(sh);
   PagedPlan p{};
+  p.few = g.rows <= kFewRows;
+  const int ctas = p.few ? 2 * sms : sms;
   // whole units where there are many, or where none is long enough to be cut
-  p.shared_out = g.units <= (long long)kManyUnits * sms && g.units <= kUnitsPerThread * 384 && max_tiles > kMinTiles;
-  p.ctas = p.shared_out ? sms : (int)std::min<long long>(sms, g.units);
-  p.launches = p.shared_out && sms > 1 ? 2 : 1;
+  p.shared_out = g.units <= std::min((long long)kManyUnits * ctas, (long long)kMaxShared) && max_tiles > kMinTiles;
+  p.ctas = p.shared_out ? ctas : (int)std::min<long long>(ctas, g.units);
+  p.launches = p.shared_out && ctas > 1 ? 2 : 1;
   // the same for every window, so that one workspace serves a model's layers
-  p.total = kWorkspaceHeader + 2 * (size_t)sms * (sizeof(Piece) + g.rows * ((size_t)sh.d * 4 + 8));
+  p.total = kWorkspaceHeader + 2 * (size_t)ctas * (sizeof(Piece) + g.rows * ((size_t)sh.d * 4 + 8));
   return p;
+}
+
+template <int D, int PAGE, bool KV4, int NT>
+cudaError_t launch_few(const Params &prm, const PagedPlan &plan, cudaStream_t stream) {
+  constexpr auto kern = paged_few<D, PAGE, KV4, NT>;
+  constexpr uint32_t kBytes = FewSmem<D, NT>::kBytes;
+  cudaError_t err = set_smem_once<kern>(kBytes);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kern, dim3((unsigned)plan.ctas), kFewThreads, kBytes, stream, prm);
 }
 
 template <int D, int PAGE, bool KV4>
@@ -1008,6 +1494,14 @@ cudaError_t launch_typed(const Shape &sh, const PagedPlan &plan, const PagedArgs
   prm.piece = reinterpret_cast<Piece *>(ws);
   prm.part_o = reinterpret_cast<float *>(ws + slots * sizeof(Piece));
   prm.part_ml = reinterpret_cast<float2 *>(prm.part_o + slots * g.rows * D);
+  auto join = [&](cudaError_t e) {
+    if (e != cudaSuccess || plan.launches == 1) return e;
+    constexpr int kWarps = kMergeThreads / 32;
+    return launch_pdl(paged_merge<D>, dim3((unsigned)(plan.ctas - 1), (unsigned)((g.rows + kWarps - 1) / kWarps)), kMergeThreads,
+                      0, stream, prm);
+  };
+  if (plan.few)
+    return join(g.rows <= 8 ? launch_few<D, PAGE, KV4, 1>(prm, plan, stream) : launch_few<D, PAGE, KV4, 2>(prm, plan, stream));
   constexpr auto kern = paged_attn<D, PAGE, KV4>;
   cudaError_t err = set_smem_once<kern>(C::kAlloc);
   if (err != cudaSuccess) return err;
@@ -1023,11 +1517,7 @@ cudaError_t launch_typed(const Shape &sh, const PagedPlan &plan, const PagedArgs
     if ((err = make_blk_tensor_map(&bk, a.blk_k, tokens, sh.Hkv, D, prm.box_blk)) != cudaSuccess) return err;
     if ((err = make_blk_tensor_map(&bv, a.blk_v, tokens, sh.Hkv, D, prm.box_blk)) != cudaSuccess) return err;
   }
-  err = launch_pdl(kern, dim3((unsigned)plan.ctas), C::kThreads, C::kAlloc, stream, prm, q, k, v, bk, bv);
-  if (err != cudaSuccess || plan.launches == 1) return err;
-  constexpr int kWarps = kMergeThreads / 32;
-  return launch_pdl(paged_merge<D>, dim3((unsigned)(plan.ctas - 1), (unsigned)((g.rows + kWarps - 1) / kWarps)), kMergeThreads, 0,
-                    stream, prm);
+  return join(launch_pdl(kern, dim3((unsigned)plan.ctas), C::kThreads, C::kAlloc, stream, prm, q, k, v, bk, bv));
 }
 
 template <bool KV4>
