@@ -193,13 +193,16 @@ __device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &f
 // The walk of a CTA through its units; every role walks the same way.
 template <bool KV4, int PAGE>
 struct Walk {
-  const Params &prm;
   int u, off, left;  // next unit, its first tile, tiles left of the share
   Keys ks;           // the current piece: tiles [t0, t0 + nt) of its unit
   Limits first, last;
   int unit, t0, nt;
-  __device__ __forceinline__ Walk(const Params &p, int u0, int off0, int left0) : prm(p), u(u0), off(off0), left(left0), unit(0), t0(0), nt(0) {}
-  __device__ __forceinline__ bool next(bool report = false) {
+  __device__ __forceinline__ void start(const int *share) {
+    u = share[0];
+    off = share[1];
+    left = share[2];
+  }
+  __device__ __forceinline__ bool next(const Params &prm, bool report = false) {
     while (u < prm.units && left > 0) {
       unit = u;
       ks = unit_keys<KV4, PAGE>(prm, u, first, last, report);
@@ -221,7 +224,7 @@ struct Walk {
 
   // Page e of tile t: logical and physical; lp = -1 where the list has ended, phys = -1
   // where the page cannot be read.
-  __device__ __forceinline__ void page_at(int t, int e, int &lp, int &phys) const {
+  __device__ __forceinline__ void page_at(const Params &prm, int t, int e, int &lp, int &phys) const {
     constexpr int PPT = kBN / PAGE;
     const Shape &sh = prm.sh;
     const int i = t * PPT + e;
@@ -237,7 +240,7 @@ struct Walk {
     if (lp >= 0) phys = (int)physical_page(sh, ks.s, lp);
   }
   // A page whose every token every row sees.
-  __device__ __forceinline__ bool page_full(int lp, int phys) const {
+  __device__ __forceinline__ bool page_full(const Params &prm, int lp, int phys) const {
     const int pb = lp * PAGE;
     return phys >= 0 && pb + PAGE <= ks.n && (KV4 || pb + PAGE <= prm.a.sinks || pb >= last.lb);
   }
@@ -253,7 +256,7 @@ struct Walk {
     return u0;
   }
   // Writes the table entry of tile t (a whole warp; lane e < PPT holds page e).
-  __device__ __forceinline__ void put_table(int *tab, int t, int lane, int lp, int phys) const {
+  __device__ __forceinline__ void put_table(const Params &prm, int *tab, int t, int lane, int lp, int phys) const {
     constexpr int PPT = kBN / PAGE;
     if (t >= ks.pt) {
       bool full;
@@ -267,7 +270,7 @@ struct Walk {
     } else {
       if (lane < PPT && lp != -1 && phys < 0) raise_status(prm.a.status, kStatusBadIndex);
       if (lane < PPT) tab[lane] = phys >= 0 ? lp * PAGE : kNever;
-      const bool full = __all_sync(0xffffffffu, lane >= PPT || page_full(lp, phys));
+      const bool full = __all_sync(0xffffffffu, lane >= PPT || page_full(prm, lp, phys));
       if (lane == 0) {
         tab[8] = full ? 1 : 0;
         tab[9] = ks.n;
@@ -422,7 +425,8 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);
-  Walk<KV4, PAGE> walk(prm, scan[0], scan[1], scan[2]);
+  Walk<KV4, PAGE> walk;
+  walk.start(scan);
 
   // Parity waits.  A wait names one of a barrier's phases, and must be made when the
   // phase before it has completed and the one after it cannot have.  k counts the CTA's
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     // ---------------------------------------------------------------- queries --
     int it = 0;
     if (lane == 0) {
-      while (walk.next(!prm.shared_out)) {  // (the scan has reported bad lengths)
+      while (walk.next(prm, !prm.shared_out)) {  // (the scan has reported bad lengths)
         if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, ctx)) break;
         mbar_arrive_expect_tx(q_full, (uint32_t)prm.bpt * sh.G * 128u * C::kHalves);
         for (int hf = 0; hf < C::kHalves; ++hf)
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       // S of the next tile of the walk, if there is one
       auto issue_s = [&]() {
         if (s_left == 0) {
-          more = more && ahead.next();
+          more = more && ahead.next(prm);
           if (!more) return true;
           s_left = ahead.nt;
           ++s_it;
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       };
       ok = issue_s() && issue_s();
       int k = 0;
-      for (int it = 0; ok && walk.next(); ++it) {
+      for (int it = 0; ok && walk.next(prm); ++it) {
         for (int j = 0; ok && j < walk.nt; ++j, ++k) {
           const int st = k % ST;
           ok = issue_s() && mbar_wait(p_full(k), (k / 3) & 1, ctx) && mbar_wait(v_full(st), (k / ST) & 1, ctx);
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         prm.piece[2 * blockIdx.x].unit = -1;
         prm.piece[2 * blockIdx.x + 1].unit = -1;
       }
-      for (; alive && walk.next(); ++it) {
+      for (; alive && walk.next(prm); ++it) {
         const Keys &ks = walk.ks;
         const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
         const Limits all{walk.first.lb, walk.last.hi, walk.last.sk};  // keys that some row may see
@@ -723,18 +727,18 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     const uint32_t ring = base + (isv ? C::kOffV : C::kOffK);
     int k = 0, told = 0;  // tiles issued; tiles announced (copies by threads are, one tile late)
     bool ok = true;
-    while (ok && walk.next()) {
+    while (ok && walk.next(prm)) {
       const Keys &ks = walk.ks;
       int lp = -1, phys = -1;
-      if (lane < PPT) walk.page_at(walk.t0, lane, lp, phys);
+      if (lane < PPT) walk.page_at(prm, walk.t0, lane, lp, phys);
       for (int j = 0; j < walk.nt; ++j, ++k) {
         const int st = k % ST, t = walk.t0 + j;
         int lp1 = -1, phys1 = -1;  // the next tile's pages, fetched before this tile's wait
-        if (j + 1 < walk.nt && lane < PPT) walk.page_at(t + 1, lane, lp1, phys1);
+        if (j + 1 < walk.nt && lane < PPT) walk.page_at(prm, t + 1, lane, lp1, phys1);
         if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (!isv) {
-          walk.put_table(table(k), t, lane, lp, phys);
+          walk.put_table(prm, table(k), t, lane, lp, phys);
           __syncwarp();
           if (lane == 0) mbar_arrive(tab_full(k));
         }
@@ -829,14 +833,14 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       ++gathered;
       return ok;
     };
-    while (ok && walk.next()) {
+    while (ok && walk.next(prm)) {
       const Keys &ks = walk.ks;
       // pages of the tiles j, j + 1, j + 2 of the piece: lane e holds page e
       int lp[3], ph[3];
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         lp[i] = ph[i] = -1;
-        if (i < walk.nt && lane < PPT) walk.page_at(walk.t0 + i, lane, lp[i], ph[i]);
+        if (i < walk.nt && lane < PPT) walk.page_at(prm, walk.t0 + i, lane, lp[i], ph[i]);
       }
       auto load = [&](int slot, int phys) {
         const uint32_t dst = base + rawring + slot * C::kRaw;
@@ -860,14 +864,14 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         const int st = k % ST, t = walk.t0 + j;
         const bool blk = t >= ks.pt;
         int lp3 = -1, ph3 = -1;
-        if (j + 3 < walk.nt && lane < PPT) walk.page_at(t + 3, lane, lp3, ph3);
+        if (j + 3 < walk.nt && lane < PPT) walk.page_at(prm, t + 3, lane, lp3, ph3);
         cp_async_wait<1>();
         if (!gather()) break;  // everybody's part of tile j is there, and tile j - 1 is read
         load((k + 2) % 3, ph[2]);
         if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (warp == 10) {
-          walk.put_table(table(k), t, lane, lp[0], ph[0]);
+          walk.put_table(prm, table(k), t, lane, lp[0], ph[0]);
           __syncwarp();
           if (lane == 0) mbar_arrive(tab_full(k));
         }
@@ -929,8 +933,8 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
 
 // ------------------------------------------------------------- few rows ----
 // Units of at most 16 query rows (decoding) are bound by the cache's bytes: a 128-row MMA
-// would idle on them.  Here a warp takes 16 keys of each tile straight from global
-// memory into the fragments of mma.m16n8k16, with no shared memory between:
+// would idle on them.  Here every warp works alone on 16 keys at a time, which come into its
+// own ring in shared memory several steps ahead, with mma.m16n8k16:
 //   S^T = K Q^T  (16 keys x 8 rows; the order of the contraction over d is free, so a
 //                 lane's K fragments are 16 contiguous bytes)
 //   O^T += V^T P^T  (d x 8 rows; the order of d over the M rows is free, so a lane's V
@@ -939,7 +943,6 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
 // P goes from the accumulators' layout to the operand's by a transposing 8x8 move.  P is
 // taken as the sum of two bf16 numbers (17 bits): the second product is free here.
 // A lane owns the maxima and sums of the rows 2t, 2t + 1 of its column.
-constexpr int kFewThreads = 256;
 constexpr int kFewRows = 16;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -956,16 +959,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_stream(const uint2 *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_stream(const uint32_t *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
@@ -998,6 +991,8 @@ struct KeysBf16 {
   }
   // first element of the four of a lane in step j of the contraction
   static __device__ __forceinline__ int k_at(int t, int j) { return (t + 4 * (j >> 1)) * 8 + 4 * (j & 1); }
+  __device__ __forceinline__ void k_begin() {}
+  __device__ __forceinline__ void v_begin(uint32_t) {}
   __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) const {
     a[0] = k[0][2 * j]; a[1] = k[1][2 * j]; a[2] = k[0][2 * j + 1]; a[3] = k[1][2 * j + 1];
   }
@@ -1008,69 +1003,139 @@ struct KeysBf16 {
     a[3] = __byte_perm(v[2][i], v[3][i], 0x7632);
   }
 };
+// The same fragments out of a warp's ring in shared memory.  A slot holds 16 keys: K rows,
+// then V rows, of a bf16 cache in 16-byte chunks whose places are permuted by row so that
+// the lanes' 16-byte reads spread over the banks.
 template <int D>
-struct KeysKv4 {
-  static constexpr int KWords = D / 32, VWords = D / 64;  // packed words of a lane per key
-  uint32_t k[2][KWords], v[4][VWords];
-  uint16_t sk[2], sv[4];
-  __device__ __forceinline__ void load_k(const uint8_t *row, const __nv_bfloat16 *sc, int g, int t, uint32_t on) {
+struct RingBf16 {
+  static constexpr int kRow = 2 * D, kSide = 16 * kRow, kSlot = 2 * kSide;
+  static constexpr int kChunks = D / 8;  // of a row
+  static __device__ __forceinline__ int k_place(int key, int c) { return key * kRow + ((c ^ ((key & 1) << 2)) << 4); }
+  static __device__ __forceinline__ int v_place(int key, int c) {
+    return key * kRow + ((c ^ ((key & 2) << 1) ^ ((key & 4) >> 2)) << 4);
+  }
+  static __device__ __forceinline__ void fetch(uint32_t dst, const PagedArgs &a, long long row, int lane) {
+#pragma unroll
+    for (int i = 0; i < 16 * kChunks / 32; ++i) {
+      const int e = lane + 32 * i, key = e / kChunks, c = e % kChunks;
+      cp_async16(dst + k_place(key, c), a.k + (row + key) * D + 8 * c);
+      cp_async16(dst + kSide + v_place(key, c), a.v + (row + key) * D + 8 * c);
+    }
+  }
+  static __device__ __forceinline__ int k_at(int t, int j) { return KeysBf16<D>::k_at(t, j); }
+  const unsigned char *at;
+  int g, t;
+  uint4 w[2];
+  __device__ __forceinline__ void k_begin() {}
+  __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) {
+    if ((j & 1) == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4 *>(at + k_place(g + 8 * i, t + 2 * j));
+    }
+    if ((j & 1) == 0) {
+      a[0] = w[0].x; a[1] = w[1].x; a[2] = w[0].y; a[3] = w[1].y;
+    } else {
+      a[0] = w[0].z; a[1] = w[1].z; a[2] = w[0].w; a[3] = w[1].w;
+    }
+  }
+  uint4 v[4];
+  uint32_t on;
+  __device__ __forceinline__ void v_begin(uint32_t on_) { on = on_; }
+  __device__ __forceinline__ void v_frag(int i, uint32_t (&a)[4]) {
+    if ((i & 3) == 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int key = 2 * t + (q & 1) + 4 * (q & 2);
+        v[q] = *reinterpret_cast<const uint4 *>(at + kSide + v_place(key, (D / 64) * g + (i >> 2)));
+        if (!((on >> key) & 1u)) v[q] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    uint32_t x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = (i & 3) == 0 ? v[q].x : (i & 3) == 1 ? v[q].y : (i & 3) == 2 ? v[q].z : v[q].w;
+    a[0] = __byte_perm(x[0], x[1], 0x5410);
+    a[1] = __byte_perm(x[0], x[1], 0x7632);
+    a[2] = __byte_perm(x[2], x[3], 0x5410);
+    a[3] = __byte_perm(x[2], x[3], 0x7632);
+  }
+};
+template <int D>
+struct RingKv4 {
+  static constexpr int GR = D / kKv4Group;
+  static constexpr int kCodes = 16 * D / 2, kScales = 16 * GR * 2;  // bytes of a side
+  static constexpr int kSide = kCodes + kScales, kSlot = 2 * kSide;
+  static __device__ __forceinline__ void fetch(uint32_t dst, const PagedArgs &a, long long row, int lane) {
+#pragma unroll
+    for (int i = 0; i < kCodes / 512; ++i) {
+      const int e = 16 * (lane + 32 * i);
+      cp_async16(dst + e, a.kv4.k + row * (D / 2) + e);
+      cp_async16(dst + kSide + e, a.kv4.v + row * (D / 2) + e);
+    }
+    const int side = lane >> 4, e = 16 * (lane & 15);
+    if (e < kScales)
+      cp_async16(dst + side * kSide + kCodes + e, reinterpret_cast<const unsigned char *>((side ? a.kv4.vs : a.kv4.ks) + row * GR) + e);
+  }
+  static __device__ __forceinline__ int k_at(int t, int j) { return (D / 4) * t + 4 * j; }
+  const unsigned char *at;
+  int g, t;
+  uint32_t k[2][D / 32], v[4][D / 64];
+  __nv_bfloat162 s8[2], m24[2];
+  static __device__ __forceinline__ uint32_t scale(const unsigned char *p) { return *reinterpret_cast<const uint16_t *>(p); }
+  __device__ __forceinline__ void constants(int i, uint32_t lo, uint32_t hi) {
+    const uint32_t x = lo | (hi << 16);
+    kv4_constants(*reinterpret_cast<const __nv_bfloat162 *>(&x), s8[i], m24[i]);
+  }
+  __device__ __forceinline__ void k_begin() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = g + 8 * i;
-      const bool o = (on >> key) & 1u;
-      sk[i] = 0;
-#pragma unroll
-      for (int w = 0; w < KWords; ++w) k[i][w] = 0x88888888u;
-      if (!o) continue;
+      const unsigned char *p = at + key * (D / 2) + t * (D / 8);
       if constexpr (D == 128) {
-        const uint4 x = ld_stream(reinterpret_cast<const uint4 *>(row + key * (D / 2)) + t);
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
         k[i][0] = x.x; k[i][1] = x.y; k[i][2] = x.z; k[i][3] = x.w;
       } else {
-        const uint2 x = ld_stream(reinterpret_cast<const uint2 *>(row + key * (D / 2)) + t);
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
         k[i][0] = x.x; k[i][1] = x.y;
       }
-      sk[i] = __ldg(reinterpret_cast<const uint16_t *>(sc) + key * (D / kKv4Group) + t * (D / 4) / kKv4Group);
+      const uint32_t sc = scale(at + kCodes + 2 * (key * GR + t * (D / 4) / kKv4Group));
+      constants(i, sc, sc);
     }
   }
-  __device__ __forceinline__ void load_v(const uint8_t *row, const __nv_bfloat16 *sc, int g, int t, uint32_t on) {
+  __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = kv4_pair(k[i][j >> 1], 2 * (j & 1), s8[i], m24[i]);
+      a[i + 2] = kv4_pair(k[i][j >> 1], 2 * (j & 1) + 1, s8[i], m24[i]);
+    }
+  }
+  __device__ __forceinline__ void v_begin(uint32_t on) {
+    uint32_t sc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = 2 * t + (i & 1) + 4 * (i & 2);
-      sv[i] = 0;
-#pragma unroll
-      for (int w = 0; w < VWords; ++w) v[i][w] = 0x88888888u;
-      if (!((on >> key) & 1u)) continue;
+      const unsigned char *p = at + kSide + key * (D / 2) + g * (D / 16);
       if constexpr (D == 128) {
-        const uint2 x = ld_stream(reinterpret_cast<const uint2 *>(row + key * (D / 2)) + g);
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
         v[i][0] = x.x; v[i][1] = x.y;
       } else {
-        v[i][0] = ld_stream(reinterpret_cast<const uint32_t *>(row + key * (D / 2)) + g);
+        v[i][0] = *reinterpret_cast<const uint32_t *>(p);
       }
-      sv[i] = __ldg(reinterpret_cast<const uint16_t *>(sc) + key * (D / kKv4Group) + g * (D / 8) / kKv4Group);
-    }
-  }
-  static __device__ __forceinline__ int k_at(int t, int j) { return (D / 4) * t + 4 * j; }
-  static __device__ __forceinline__ __nv_bfloat162 pair(uint16_t a, uint16_t b) {
-    const uint32_t x = (uint32_t)a | ((uint32_t)b << 16);
-    return *reinterpret_cast<const __nv_bfloat162 *>(&x);
-  }
-  __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) const {
+      sc[i] = scale(at + kSide + kCodes + 2 * (key * GR + g * (D / 8) / kKv4Group));
+      if (!((on >> key) & 1u)) {  // code 8 with scale 0 is the value 0
+        sc[i] = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      __nv_bfloat162 s8, m24;
-      kv4_constants(pair(sk[i], sk[i]), s8, m24);
-      a[i] = kv4_pair(k[i][j >> 1], 2 * (j & 1), s8, m24);
-      a[i + 2] = kv4_pair(k[i][j >> 1], 2 * (j & 1) + 1, s8, m24);
+        for (int w = 0; w < D / 64; ++w) v[i][w] = 0x88888888u;
+      }
     }
+    constants(0, sc[0], sc[1]);
+    constants(1, sc[2], sc[3]);
   }
-  __device__ __forceinline__ void v_frag(int i, uint32_t (&a)[4]) const {
+  __device__ __forceinline__ void v_frag(int i, uint32_t (&a)[4]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      __nv_bfloat162 s8, m24;
-      kv4_constants(pair(sv[2 * p], sv[2 * p + 1]), s8, m24);
       const uint32_t x = v[2 * p][i >> 2], y = v[2 * p + 1][i >> 2];
-      a[2 * p] = kv4_pair(__byte_perm(x, y, 0x5410), i & 3, s8, m24);
-      a[2 * p + 1] = kv4_pair(__byte_perm(x, y, 0x7632), i & 3, s8, m24);
+      a[2 * p] = kv4_pair(__byte_perm(x, y, 0x5410), i & 3, s8[p], m24[p]);
+      a[2 * p + 1] = kv4_pair(__byte_perm(x, y, 0x7632), i & 3, s8[p], m24[p]);
     }
   }
 };
@@ -1084,11 +1149,12 @@ struct FewState {
 
 // One step: 16 keys of fragments `f`; `hid` bit 4 n + 2 i + e: key g + 8 i is hidden from row 8 n + 2t + e.
 template <int D, int NT, class F>
-__device__ __forceinline__ void few_scores(const F &f, const uint2 *qf, int lane, float (&x)[NT][4]) {
+__device__ __forceinline__ void few_scores(F &f, const uint2 *qf, int lane, float (&x)[NT][4]) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+  f.k_begin();
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
     uint32_t a[4];
@@ -1152,7 +1218,7 @@ __device__ __forceinline__ void few_softmax(FewState<D, NT> &st, float (&x)[NT][
   }
 }
 template <int D, int NT, class F>
-__device__ __forceinline__ void few_values(const F &f, FewState<D, NT> &st, const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2]) {
+__device__ __forceinline__ void few_values(F &f, FewState<D, NT> &st, const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2]) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     uint32_t a[4];
@@ -1165,50 +1231,58 @@ __device__ __forceinline__ void few_values(const F &f, FewState<D, NT> &st, cons
   }
 }
 
-template <int D, int NT>
-struct FewSmem {
-  static constexpr uint32_t kQ = 0;                                   // fragments [NT][D/16][32] x 8 bytes
-  static constexpr uint32_t kML = kQ + NT * (D / 16) * 32 * 8;         // [8 warps][8 NT rows] (m, l)
-  static constexpr uint32_t kO = kML + 8 * 8 * NT * 8;                 // [8 warps][8 NT rows][D + 4]
+template <int D, bool KV4, int NT>
+struct FewCfg {
+  using Ring = typename std::conditional<KV4, RingKv4<D>, RingBf16<D>>::type;
+  // two CTAs an SM.  The bf16 cache needs bytes in flight (8 warps x 3 steps of 8 KB an SM),
+  // the 4-bit one warps to unpack (16, 4 steps of 2.3 KB each)
+  static constexpr int kWarps = KV4 ? 8 : 4, kSteps = KV4 ? 4 : 3;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kPerTile = 8 / kWarps;                          // steps of a warp per tile
+  static constexpr uint32_t kQ = 0;                                    // fragments [NT][D/16][32] x 8 bytes
+  static constexpr uint32_t kML = kQ + NT * (D / 16) * 32 * 8;          // [warps][8 NT rows] (m, l)
+  static constexpr uint32_t kRing = kML + kWarps * 8 * NT * 8;         // [warps][steps] slots
+  static constexpr uint32_t kO = kRing;                                // [warps][8 NT rows][D + 4], after the ring's use
   static constexpr int kRow = D + 4;                                   // spreads the rows over the banks
-  static constexpr uint32_t kBytes = kO + 8 * 8 * NT * kRow * 4;
+  static constexpr uint32_t kRingBytes = kWarps * kSteps * Ring::kSlot, kOBytes = kWarps * 8 * NT * kRow * 4;
+  static constexpr uint32_t kBytes = kRing + (kRingBytes > kOBytes ? kRingBytes : kOBytes);
 };
 
 template <int D, int PAGE, bool KV4, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 || KV4 ? 2 : 1) paged_few(const __grid_constant__ Params prm) {
-  using M = FewSmem<D, NT>;
+__global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(const __grid_constant__ Params prm) {
+  using M = FewCfg<D, KV4, NT>;
+  constexpr int W = M::kWarps;
   extern __shared__ unsigned char smem_raw[];
   uint2 *qf = reinterpret_cast<uint2 *>(smem_raw + M::kQ);
   float2 *ml = reinterpret_cast<float2 *>(smem_raw + M::kML);
   float *ow = reinterpret_cast<float *>(smem_raw + M::kO);
-  __shared__ int scan[3], sums[kFewThreads / 32];
+  __shared__ int scan[3], sums[W], more_units;
+  __shared__ Walk<KV4, PAGE> walk;  // the current piece, read where it is needed: registers are short
   const Shape &sh = prm.sh;
   const PagedArgs &a = prm.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  cta_share<KV4, PAGE, kFewThreads>(prm, scan, sums);
-  Walk<KV4, PAGE> walk(prm, scan[0], scan[1], scan[2]);
-  if (threadIdx.x == 0 && prm.shared_out) prm.piece[2 * blockIdx.x].unit = prm.piece[2 * blockIdx.x + 1].unit = -1;
-  const int sub = warp;  // this warp's 16 keys of each tile
-  while (walk.next(!prm.shared_out && threadIdx.x == 0)) {
+  cta_share<KV4, PAGE, M::kThreads>(prm, scan, sums);
+  if (threadIdx.x == 0) {
+    walk.start(scan);
+    if (prm.shared_out) prm.piece[2 * blockIdx.x].unit = prm.piece[2 * blockIdx.x + 1].unit = -1;
+  }
+  for (;;) {
+    if (threadIdx.x == 0) more_units = walk.next(prm, !prm.shared_out);
+    __syncthreads();
+    if (!more_units) break;
     const Keys &ks = walk.ks;
     // queries in the order of the contraction
-    for (int e = threadIdx.x; e < NT * (D / 16) * 32; e += kFewThreads) {
+    for (int e = threadIdx.x; e < NT * (D / 16) * 32; e += M::kThreads) {
       const int ln = e & 31, j = e / 32 % (D / 16), r = 8 * (e / 32 / (D / 16)) + (ln >> 2);
       uint2 q = make_uint2(0, 0);
-      const int at = KV4 ? KeysKv4<D>::k_at(ln & 3, j) : KeysBf16<D>::k_at(ln & 3, j);
+      const int at = M::Ring::k_at(ln & 3, j);
       if (r < ks.rows)
         q = *reinterpret_cast<const uint2 *>(a.q + (((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G) * D + at);
       qf[e] = q;
     }
     __syncthreads();
-    Limits lim[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) lim[n][e] = row_limits<KV4>(a, ks.n, ks.b0 + (8 * n + 2 * t4 + e) / sh.G);
-    const Limits all{walk.first.lb, walk.last.hi, walk.last.sk};
     FewState<D, NT> st;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -1224,85 +1298,77 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 || KV4 ? 2 : 1) paged_few
     }
     // which keys of the 16 at position `pos` (none at kNever) any row sees; bits of `hid` as above
     auto masks = [&](int pos, int end, uint32_t &on, uint32_t &hid) {
-      on = visible(pos, 16, end, all);
+      on = 0xffffu;
       hid = 0;
-      const bool full = pos != kNever && pos + 16 <= end &&
-                        (KV4 || pos + 16 <= walk.first.sk || (pos >= walk.last.lb && pos + 15 <= walk.first.hi));
-      if (full) return;
+      if (pos != kNever && pos + 16 <= end &&
+          (KV4 || pos + 16 <= walk.first.sk || (pos >= walk.last.lb && pos + 15 <= walk.first.hi)))
+        return;
+      on = visible(pos, 16, end, Limits{walk.first.lb, walk.last.hi, walk.last.sk});
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t v = visible(pos, 16, end, lim[n][e]);
+          const uint32_t v = visible(pos, 16, end, row_limits<KV4>(a, ks.n, ks.b0 + (8 * n + 2 * t4 + e) / sh.G));
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (!((v >> (g + 8 * i)) & 1u)) hid |= 1u << (4 * n + 2 * i + e);
         }
     };
-    // ---- tiles of pages: page ids of 32 tiles at a time, a lane each
-    using F = typename std::conditional<KV4, KeysKv4<D>, KeysBf16<D>>::type;
-    constexpr int kDeep = KV4 ? 2 : 1;  // steps in flight ahead of the one being worked on
-    const int np = max(0, min(walk.nt, ks.pt - walk.t0));
-    F f[kDeep];
-    uint32_t on[kDeep], hid[kDeep];
+    // ---- tiles of pages.  Step i of a warp is 16 keys of tile i / kPerTile; the pages of 32
+    //      steps are looked up at a time, a lane each.
+    const int np = max(0, min(walk.nt, ks.pt - walk.t0)) * M::kPerTile, head = ks.h, n_ctx = ks.n;
+    auto sub_of = [&](int i) { return warp + W * (i % M::kPerTile); };  // its place in the tile, in 16 keys
     int lps = -1, phs = -1;
-    auto row_of = [&](int j, int &pos) {  // row of the first of the warp's 16 keys in tile j of the piece
-      if ((j & 31) == 0) {
-        lps = phs = -1;
-        if (j + lane < np) walk.page_at(walk.t0 + j + lane, 16 * sub / PAGE, lps, phs);
-        if (lps != -1 && phs < 0 && (16 * sub) % PAGE == 0) raise_status(a.status, kStatusBadIndex);
-      }
-      const int lp = __shfl_sync(0xffffffffu, lps, j & 31), ph = __shfl_sync(0xffffffffu, phs, j & 31);
-      pos = ph >= 0 ? lp * PAGE + 16 * sub % PAGE : kNever;
-      return ((long long)max(ph, 0) * sh.Hkv + ks.h) * PAGE + 16 * sub % PAGE;
-    };
-    long long row[kDeep];
-    auto issue_k = [&](int d, int j) {
-      int pos;
-      row[d] = row_of(j, pos);
-      masks(pos, ks.n, on[d], hid[d]);
-      if constexpr (KV4)
-        f[d].load_k(a.kv4.k + row[d] * (D / 2), a.kv4.ks + row[d] * (D / kKv4Group), g, t4, on[d]);
-      else
-        f[d].load_k(a.k + row[d] * D, D, g, t4, on[d]);
-    };
-    auto issue_v = [&](int d) {
-      if constexpr (KV4)
-        f[d].load_v(a.kv4.v + row[d] * (D / 2), a.kv4.vs + row[d] * (D / kKv4Group), g, t4, on[d]);
-      else
-        f[d].load_v(a.v + row[d] * D, D, g, t4, on[d]);
-    };
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d)
-      if (d < np) {
-        issue_k(d, d);
-        issue_v(d);
-      }
-    for (int j0 = 0; j0 < np; j0 += kDeep) {
-#pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        if (j0 + d >= np) break;
-        float x[NT][4];
-        uint32_t ph[NT][2], pl[NT][2];
-        const bool some = on[d] != 0;  // the same in every lane
-        const uint32_t h = hid[d];
-        if (some) few_scores<D, NT>(f[d], qf, lane, x);
-        // K of the next step is on its way while this step's values are worked on, its V
-        // during the next scores
-        const bool more = j0 + d + kDeep < np;
-        if (more) issue_k(d, j0 + d + kDeep);
-        if (some) {
-          few_softmax<D, NT>(st, x, h, sh.sl2, ph, pl);
-          few_values<D, NT>(f[d], st, ph, pl);
+    const uint32_t ring = smem_addr(smem_raw) + M::kRing + warp * (M::kSteps * M::Ring::kSlot);
+    int pos[M::kSteps];  // position of the step's first key
+    auto issue = [&](int slot, int i) {
+      if (i < np) {
+        if ((i & 31) == 0) {
+          lps = phs = -1;
+          const int e = i + lane;
+          if (e < np) walk.page_at(prm, walk.t0 + e / M::kPerTile, 16 * sub_of(e) / PAGE, lps, phs);
+          if (lps != -1 && phs < 0) raise_status(a.status, kStatusBadIndex);
         }
-        if (more) issue_v(d);
+        const int lp = __shfl_sync(0xffffffffu, lps, i & 31), ph = __shfl_sync(0xffffffffu, phs, i & 31);
+        const int in_page = 16 * sub_of(i) % PAGE;
+        pos[slot] = ph >= 0 ? lp * PAGE + in_page : kNever;
+        if (ph >= 0 && pos[slot] < n_ctx)
+          M::Ring::fetch(ring + slot * M::Ring::kSlot, a, ((long long)ph * sh.Hkv + head) * PAGE + in_page, lane);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < M::kSteps; ++d) issue(d, d);
+    for (int i0 = 0; i0 < np; i0 += M::kSteps) {
+#pragma unroll
+      for (int d = 0; d < M::kSteps; ++d) {
+        if (i0 + d < np) {
+          uint32_t on, hid;
+          masks(pos[d], n_ctx, on, hid);
+          cp_async_wait<M::kSteps - 1>();
+          __syncwarp();  // every lane's part of the step is there
+          if (on) {      // the same in every lane
+            float x[NT][4];
+            uint32_t ph[NT][2], pl[NT][2];
+            typename M::Ring f;
+            f.at = smem_raw + M::kRing + (warp * M::kSteps + d) * M::Ring::kSlot;
+            f.g = g;
+            f.t = t4;
+            few_scores<D, NT>(f, qf, lane, x);
+            f.v_begin(on);
+            few_softmax<D, NT>(st, x, hid, sh.sl2, ph, pl);
+            few_values<D, NT>(f, st, ph, pl);
+          }
+          __syncwarp();  // every lane has read the slot
+          issue(d, i0 + d + M::kSteps);
+        }
       }
     }
     // ---- tiles of block tokens (bf16)
-    for (int j = np; j < walk.nt; ++j) {
+    for (int i = np; i < walk.nt * M::kPerTile; ++i) {
       int u_end;
       bool fl;
-      const int u = walk.blk_tile(walk.t0 + j, u_end, fl) + 16 * sub;
+      const int u = walk.blk_tile(walk.t0 + i / M::kPerTile, u_end, fl) + 16 * sub_of(i);
       if (u >= u_end) continue;
       uint32_t on0, hid0, ph[NT][2], pl[NT][2];
       masks(ks.n + u, ks.n + u_end, on0, hid0);
@@ -1337,6 +1403,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 || KV4 ? 2 : 1) paged_few
       few_softmax<D, NT>(st, x, hid0, sh.sl2, ph, pl);
       few_values<D, NT>(b, st, ph, pl);
     }
+    cp_async_wait<0>();
+    __syncthreads();  // the rings give way to the warps' O
     // ---- join the warps: sums over the lanes' keys, then (m, l, O) of each warp
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -1359,17 +1427,17 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 || KV4 ? 2 : 1) paged_few
     const bool whole = walk.begins() && walk.ends();
     const int slot = 2 * blockIdx.x + (walk.begins() ? 1 : 0);
     if (!whole && threadIdx.x == 0) prm.piece[slot] = Piece{walk.unit, walk.begins(), walk.ends(), 0};
-    for (int e = threadIdx.x; e < ks.rows * (D / 4); e += kFewThreads) {
+    for (int e = threadIdx.x; e < ks.rows * (D / 4); e += M::kThreads) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float mx = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float2 v = ml[w * 8 * NT + r];
         if (v.y != 0.f) mx = fmaxf(mx, v.x);
       }
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float2 v = ml[w * 8 * NT + r];
         if (v.y == 0.f) continue;
         const float wt = v.x == -INFINITY ? 1.f : exp2f(v.x - mx);
@@ -1470,10 +1538,10 @@ PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles) {
 template <int D, int PAGE, bool KV4, int NT>
 cudaError_t launch_few(const Params &prm, const PagedPlan &plan, cudaStream_t stream) {
   constexpr auto kern = paged_few<D, PAGE, KV4, NT>;
-  constexpr uint32_t kBytes = FewSmem<D, NT>::kBytes;
-  cudaError_t err = set_smem_once<kern>(kBytes);
+  using M = FewCfg<D, KV4, NT>;
+  cudaError_t err = set_smem_once<kern>(M::kBytes);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kern, dim3((unsigned)plan.ctas), kFewThreads, kBytes, stream, prm);
+  return launch_pdl(kern, dim3((unsigned)plan.ctas), M::kThreads, M::kBytes, stream, prm);
 }
 
 template <int D, int PAGE, bool KV4>
