@@ -1478,27 +1478,42 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_consta
   const int b = rt * prm.bpt + r / sh.G;
   if (b >= block_tokens(prm.a.n_new, s, sh.B, prm.a.status, false)) return;
   constexpr int E = D / 32;
+  // the pieces: slot 2 c + 1 of CTA c = x, then slots 2 (c + 1), ... to the one that ends the
+  // unit; a lane looks at one each, so that the chain costs one round of loads per 32
+  int count = 0;
+  for (int i0 = 0;; i0 += 32) {
+    const int c = blockIdx.x + i0 + lane;
+    const bool ends = c > (int)gridDim.x || prm.piece[c == (int)blockIdx.x ? 2 * c + 1 : 2 * c].ends;
+    const uint32_t found = __ballot_sync(0xffffffffu, ends);
+    count += found ? __ffs(found) : 32;
+    if (found) break;
+  }
+  count = min(count, (int)gridDim.x + 1 - (int)blockIdx.x);  // (a call that gave up may have left no end)
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  int slot = 2 * blockIdx.x + 1;
-  for (int c = blockIdx.x; c <= (int)gridDim.x; ++c) {  // CTAs 0 .. gridDim.x
-    const size_t prow = (size_t)slot * rpt + r;
-    const float2 ml = prm.part_ml[prow];
-    const bool ends = prm.piece[slot].ends;
-    float v[E];
+  auto row_of = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * rpt + r; };
+  for (int i0 = 0; i0 < count; i0 += 8) {
+    float2 ml[8];
+    float v[8][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = prm.part_o[prow * D + lane * E + e];
-    if (ml.y != 0.f) {  // a piece without a visible key holds zeros
-      const float mn = fmaxf(M, ml.x);
-      const float sc = M == -INFINITY ? 0.f : exp2f(M - mn), wt = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mn);
-      M = mn;
-      L = fmaf(L, sc, wt * ml.y);
+    for (int i = 0; i < 8; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i >= count) continue;
+      ml[i] = prm.part_ml[row_of(i0 + i)];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], sc, wt * v[e]);
+      for (int e = 0; e < E; ++e) v[i][e] = prm.part_o[row_of(i0 + i) * D + lane * E + e];
     }
-    if (ends) break;
-    slot = 2 * (c + 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (ml[i].y == 0.f) continue;  // a piece without a visible key holds zeros
+      const float mn = fmaxf(M, ml[i].x);
+      const float sc = M == -INFINITY ? 0.f : exp2f(M - mn), wt = ml[i].x == -INFINITY ? 1.f : exp2f(ml[i].x - mn);
+      M = mn;
+      L = fmaf(L, sc, wt * ml[i].y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], sc, wt * v[i][e]);
+    }
   }
   const size_t orow = ((size_t)s * sh.B + b) * sh.Hq + (size_t)h * sh.G + r % sh.G;
   const float inv = L != 0.f ? 1.f / L : 0.f;
