@@ -63,12 +63,13 @@ struct Cfg {
   static constexpr uint32_t kRaw = kRawCodes + kBN * (D / kKv4Group) * 2;
   static constexpr uint32_t kOffRaw = kOffV + kStages * kTile;
   static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? 2 * kRawSlots * kRaw : 0);
-  static constexpr int kNumBars = 4 * kStages + kTabs + 18;
+  static constexpr int kNumBars = 4 * kStages + kTabs + 24;
   static constexpr uint32_t kOffTab = kOffBar + kNumBars * 8;      // per tile: 8 positions, flags, end
   static constexpr uint32_t kOffMisc = kOffTab + kTabs * 40;       // TMEM address, abort flag, scan result
   static constexpr uint32_t kOffM = kOffMisc + 32;                 // [128] reference maxima
   static constexpr uint32_t kOffL = kOffM + 512;                   // [128] sums on their way between groups
-  static constexpr uint32_t kAlloc = kOffL + 512 + 1024;           // room to align the base to 1 KB
+  static constexpr uint32_t kOffStop = kOffL + 512;                // [3] stops of the walk
+  static constexpr uint32_t kAlloc = kOffStop + 3 * 96 + 1024;     // room to align the base to 1 KB
   static constexpr uint32_t kTmemO = 3 * kBN;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kAlloc <= 232448, "shared memory of a CTA");
@@ -190,35 +191,13 @@ __device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &f
   return ks;
 }
 
-// The walk of a CTA through its units; every role walks the same way.
+// One stop of a CTA's walk through its units: tiles [t0, t0 + nt) of a unit.  One thread
+// works it out, the others read it in shared memory.
 template <bool KV4, int PAGE>
-struct Walk {
-  int u, off, left;  // next unit, its first tile, tiles left of the share
-  Keys ks;           // the current piece: tiles [t0, t0 + nt) of its unit
+struct Stop {
+  Keys ks;
   Limits first, last;
-  int unit, t0, nt;
-  __device__ __forceinline__ void start(const int *share) {
-    u = share[0];
-    off = share[1];
-    left = share[2];
-  }
-  __device__ __forceinline__ bool next(const Params &prm, bool report = false) {
-    while (u < prm.units && left > 0) {
-      unit = u;
-      ks = unit_keys<KV4, PAGE>(prm, u, first, last, report);
-      t0 = off;
-      nt = min(ks.tiles - off, left);
-      off = 0;
-      if (prm.shared_out) {
-        left -= nt;
-        ++u;
-      } else {
-        u += gridDim.x;
-      }
-      if (nt > 0) return true;
-    }
-    return false;
-  }
+  int unit, t0, nt;  // nt = 0: the walk is over
   __device__ __forceinline__ bool begins() const { return t0 == 0; }
   __device__ __forceinline__ bool ends() const { return t0 + nt == ks.tiles; }
 
@@ -279,6 +258,31 @@ struct Walk {
   }
 };
 
+// The walk itself: from a share (see cta_share) to its stops.
+template <bool KV4, int PAGE>
+struct Walk {
+  int u, off, left;  // next unit, its first tile, tiles left of the share
+  __device__ __forceinline__ explicit Walk(const int *share) : u(share[0]), off(share[1]), left(share[2]) {}
+  __device__ __forceinline__ bool next(const Params &prm, Stop<KV4, PAGE> &at) {
+    while (u < prm.units && left > 0) {
+      at.unit = u;
+      at.ks = unit_keys<KV4, PAGE>(prm, u, at.first, at.last, !prm.shared_out);  // (the scan has reported bad lengths)
+      at.t0 = off;
+      at.nt = min(at.ks.tiles - off, left);
+      off = 0;
+      if (prm.shared_out) {
+        left -= at.nt;
+        ++u;
+      } else {
+        u += gridDim.x;
+      }
+      if (at.nt > 0) return true;
+    }
+    at.nt = 0;
+    return false;
+  }
+};
+
 // This CTA's share, by a scan over the units' tiles: share[0..2] = its first unit, the
 // first tile of it, its number of tiles.  All threads; ends with a CTA barrier.  `sums`: an
 // int per warp.
@@ -291,18 +295,15 @@ __device__ __forceinline__ void cta_share(const Params &prm, int *share, int *su
     share[2] = prm.shared_out ? 0 : INT_MAX;
   }
   if (prm.shared_out) {
-    constexpr int kUnits = (kMaxShared + THREADS - 1) / THREADS;  // of a thread
-    const int u0 = threadIdx.x * kUnits;
-    int cnt[kUnits], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      cnt[i] = 0;
-      if (u0 + i < prm.units) {
-        Limits x, y;
-        cnt[i] = unit_keys<KV4, PAGE>(prm, u0 + i, x, y, blockIdx.x == 0).tiles;
-      }
-      mine += cnt[i];
-    }
+    const int per = (prm.units + THREADS - 1) / THREADS;  // units of a thread
+    const int u0 = threadIdx.x * per, u1 = min(u0 + per, prm.units);
+    int mine = 0;
+    auto tiles_of = [&](int u) {
+      Limits x, y;
+      return unit_keys<KV4, PAGE>(prm, u, x, y, blockIdx.x == 0).tiles;
+    };
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) mine += tiles_of(u);
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -321,14 +322,17 @@ __device__ __forceinline__ void cta_share(const Params &prm, int *share, int *su
     if (c < shares) {
       const int lo = (int)((long long)total * c / shares), hi = (int)((long long)total * (c + 1) / shares);
       int at = before + upto - mine;  // first tile of this thread's units
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if (lo >= at && lo < at + cnt[i]) {
-          share[0] = u0 + i;
-          share[1] = lo - at;
-          share[2] = hi - lo;
+      if (lo >= at && lo < at + mine) {
+#pragma unroll 1
+        for (int u = u0; u < u1; ++u) {
+          const int n = per == 1 ? mine : tiles_of(u);
+          if (lo >= at && lo < at + n) {
+            share[0] = u;
+            share[1] = lo - at;
+            share[2] = hi - lo;
+          }
+          at += n;
         }
-        at += cnt[i];
       }
     }
   }
@@ -375,6 +379,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   const uint32_t q_full = bar(kB0 + 10), q_empty = bar(kB0 + 11), o_full = bar(kB0 + 12), o_free = bar(kB0 + 13);
   // softmax threads among themselves, the loaders of K and of V among themselves (4-bit cache), the last MMA
   const uint32_t meet = bar(kB0 + 14), drain = bar(kB0 + 17);
+  auto stop_full = [&](int it) { return bar(kB0 + 18 + it % 3); };
+  auto stop_empty = [&](int it) { return bar(kB0 + 21 + it % 3); };
+  static_assert(sizeof(Stop<KV4, PAGE>) <= 96, "slot of a stop");
+  auto stop_at = [&](int it) { return reinterpret_cast<Stop<KV4, PAGE> *>(smem + C::kOffStop + (it % 3) * 96); };
   auto loaders = [&](bool isv) { return bar(kB0 + 15 + (isv ? 1 : 0)); };
   auto table = [&](int k) { return reinterpret_cast<int *>(smem + C::kOffTab + (k % kTabs) * 40); };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -409,6 +417,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     mbar_init(loaders(false), 64);
     mbar_init(loaders(true), 64);
     mbar_init(drain, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(stop_full(i), 1);
+      mbar_init(stop_empty(i), 1 + 2 * aw + 2 * kLoaders / 32);  // the issuer, softmax warps, loaders' warps
+    }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&qmap);
@@ -425,8 +437,15 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc);
-  Walk<KV4, PAGE> walk;
-  walk.start(scan);
+  // The role's next stop: waits for it, and (done) gives the last one's slot back.  False at
+  // the end of the walk, and where a wait gave up.
+  auto arrive_at = [&](int it) {
+    return mbar_wait(stop_full(it), (it / 3) & 1, ctx) && stop_at(it)->nt > 0;
+  };
+  auto leave = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(stop_empty(it));
+  };
 
   // Parity waits.  A wait names one of a barrier's phases, and must be made when the
   // phase before it has completed and the one after it cannot have.  k counts the CTA's
@@ -446,19 +465,28 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   //                        there; the next one, k + 2, needs the decision on k + 1.  Before
   //                        a unit both groups have met after the last PV, so none is skipped
   //                        that has not completed.
-  //   q_full, q_empty, o_full, o_free   once per unit, each after the one before it.
+  //   q_full, q_empty, o_full, o_free   once per stop, each after the one before it.
+  //   stop_full, stop_empty (it)   three slots: the one of stop it + 3 is written after
+  //                        every role has left stop it.  The issuer reads stop it + 2 at most
+  //                        while PV of stop it, which others wait for, is still to be sent.
   if (KV4 ? warp == 0 : warp == 11) {
-    // ---------------------------------------------------------------- queries --
-    int it = 0;
+    // ------------------------------------------------- the walk, and queries --
     if (lane == 0) {
-      while (walk.next(prm, !prm.shared_out)) {  // (the scan has reported bad lengths)
+      Walk<KV4, PAGE> walk(scan);
+      int loaded = 0;
+      for (int it = 0;; ++it) {
+        if (it >= 3 && !mbar_wait(stop_empty(it), ((it / 3) - 1) & 1, ctx)) break;
+        Stop<KV4, PAGE> &at = *stop_at(it);
+        const bool more = walk.next(prm, at);
+        mbar_arrive(stop_full(it));
+        if (!more) break;
         if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, ctx)) break;
         mbar_arrive_expect_tx(q_full, (uint32_t)prm.bpt * sh.G * 128u * C::kHalves);
         for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(base + C::kOffQ + hf * C::kHalf, &qmap, q_full, hf * 64, walk.ks.h * sh.G, walk.ks.s * sh.B + walk.ks.b0);
-        ++it;
+          tma_load_3d(base + C::kOffQ + hf * C::kHalf, &qmap, q_full, hf * 64, at.ks.h * sh.G, at.ks.s * sh.B + at.ks.b0);
+        loaded = it + 1;
       }
-      if (it > 0) mbar_wait(q_full, (it - 1) & 1, drain_ctx);  // a copy in flight lands before the CTA ends
+      if (loaded > 0) mbar_wait(q_full, (loaded - 1) & 1, drain_ctx);  // a copy in flight lands before the CTA ends
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -466,17 +494,23 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t ids = idesc_bf16(128, kBN, false, false);
       constexpr uint32_t ido = idesc_bf16(128, D, false, true);
-      Walk<KV4, PAGE> ahead = walk;  // two tiles ahead: S
-      int s_it = -1, s_left = 0, ks = 0;
+      // S runs two tiles, so up to two stops, ahead of PV: the tile counts of stops between
+      int s_it = 0, s_left = 0, ks = 0, counts[4] = {0, 0, 0, 0};
       bool more = true, ok = true;
       // S of the next tile of the walk, if there is one
       auto issue_s = [&]() {
         if (s_left == 0) {
-          more = more && ahead.next(prm);
           if (!more) return true;
-          s_left = ahead.nt;
-          ++s_it;
+          if (!mbar_wait(stop_full(s_it), (s_it / 3) & 1, ctx)) return false;
+          s_left = stop_at(s_it)->nt;
+          mbar_arrive(stop_empty(s_it));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i == (s_it & 3)) counts[i] = s_left;
+          more = s_left > 0;
+          if (!more) return true;
           if (!mbar_wait(q_full, s_it & 1, ctx)) return false;
+          ++s_it;
         }
         const int st = ks % ST;
         if (!mbar_wait(k_full(st), (ks / ST) & 1, ctx)) return false;
@@ -498,8 +532,13 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       };
       ok = issue_s() && issue_s();
       int k = 0;
-      for (int it = 0; ok && walk.next(prm); ++it) {
-        for (int j = 0; ok && j < walk.nt; ++j, ++k) {
+      for (int it = 0; ok; ++it) {
+        int nt = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == (it & 3)) nt = counts[i];
+        if (it >= s_it || nt == 0) break;
+        for (int j = 0; ok && j < nt; ++j, ++k) {
           const int st = k % ST;
           ok = issue_s() && mbar_wait(p_full(k), (k / 3) & 1, ctx) && mbar_wait(v_full(st), (k / ST) & 1, ctx);
           // the epilogue of the unit before has read O
@@ -539,12 +578,12 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         prm.piece[2 * blockIdx.x].unit = -1;
         prm.piece[2 * blockIdx.x + 1].unit = -1;
       }
-      for (; alive && walk.next(prm); ++it) {
-        const Keys &ks = walk.ks;
-        const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
-        const Limits all{walk.first.lb, walk.last.hi, walk.last.sk};  // keys that some row may see
+      for (; __all_sync(0xffffffffu, arrive_at(it)); leave(it), ++it) {
+        const Stop<KV4, PAGE> &at = *stop_at(it);
+        const Keys &ks = at.ks;
+        const int rows = ks.rows;
         float m_used = -INFINITY, l = 0.f;
-        const int k1 = k0 + walk.nt;
+        const int k1 = k0 + at.nt;
         for (int k = k0 + ((k0 ^ g) & 1); k < k1; k += 2) {
           const uint32_t sc = lt + (k % 3) * kBN;
           alive = __all_sync(0xffffffffu, mbar_wait(tab_full(k), (k / kTabs) & 1, ctx) && mbar_wait(s_full(k), (k / 3) & 1, ctx));
@@ -556,6 +595,8 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           if (!(flags & 1)) {
             const bool blk = flags & 2;
             const int end = tab[9], st = k % ST;
+            const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
+            const Limits all{at.first.lb, at.last.hi, at.last.sk};  // keys that some row may see
 #pragma unroll
             for (int w = 0; w < 4; ++w) bits[w] = visible32<PAGE>(tab, blk, w, end, mine);
             // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
@@ -602,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
               for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(y[j]));
             }
           }
-          const float tmax = r < ks.rows ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2 : -INFINITY;
+          const float tmax = r < rows ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2 : -INFINITY;
           // the reference so far, from the group of the tile before; a row past the unit's keeps none
           float m_prev = -INFINITY;
           if (k > k0) {
@@ -677,9 +718,9 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         if (!meet_all()) break;
         const float L = g == 0 ? l : l_x[r];
         const bool has = L != 0.f;  // a NaN sum counts
-        const bool whole = walk.begins() && walk.ends();
-        const int slot = 2 * blockIdx.x + (walk.begins() ? 1 : 0);
-        const bool mine_row = r < ks.rows;
+        const bool whole = at.begins() && at.ends();
+        const int slot = 2 * blockIdx.x + (at.begins() ? 1 : 0);
+        const bool mine_row = r < rows;
         const size_t orow = ((size_t)ks.s * sh.B + ks.b0 + r / sh.G) * sh.Hq + (size_t)ks.h * sh.G + r % sh.G;
         const size_t prow = (size_t)slot * ((size_t)prm.bpt * sh.G) + r;
         const float wt = whole ? (has ? 1.f / L : 0.f) : 1.f;
@@ -690,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             sh.lse_out[orow] = has ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
           }
         }
-        if (!whole && warp == 4 && lane == 0) prm.piece[slot] = Piece{walk.unit, walk.begins(), walk.ends(), 0};
+        if (!whole && warp == 4 && lane == 0) prm.piece[slot] = Piece{at.unit, at.begins(), at.ends(), 0};
 #pragma unroll
         for (int i0 = 0; i0 < D / 2; i0 += 32) {
           const int c0 = g * (D / 2) + i0;
@@ -727,18 +768,20 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     const uint32_t ring = base + (isv ? C::kOffV : C::kOffK);
     int k = 0, told = 0;  // tiles issued; tiles announced (copies by threads are, one tile late)
     bool ok = true;
-    while (ok && walk.next(prm)) {
-      const Keys &ks = walk.ks;
+    for (int it = 0; ok && __all_sync(0xffffffffu, arrive_at(it)); leave(it), ++it) {
+      const Stop<KV4, PAGE> &at = *stop_at(it);
+      const Keys &ks = at.ks;
+      const int nt = at.nt, t0 = at.t0;
       int lp = -1, phys = -1;
-      if (lane < PPT) walk.page_at(prm, walk.t0, lane, lp, phys);
-      for (int j = 0; j < walk.nt; ++j, ++k) {
-        const int st = k % ST, t = walk.t0 + j;
+      if (lane < PPT) at.page_at(prm, t0, lane, lp, phys);
+      for (int j = 0; j < nt; ++j, ++k) {
+        const int st = k % ST, t = t0 + j;
         int lp1 = -1, phys1 = -1;  // the next tile's pages, fetched before this tile's wait
-        if (j + 1 < walk.nt && lane < PPT) walk.page_at(prm, t + 1, lane, lp1, phys1);
+        if (j + 1 < nt && lane < PPT) at.page_at(prm, t + 1, lane, lp1, phys1);
         if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (!isv) {
-          walk.put_table(prm, table(k), t, lane, lp, phys);
+          at.put_table(prm, table(k), t, lane, lp, phys);
           __syncwarp();
           if (lane == 0) mbar_arrive(tab_full(k));
         }
@@ -746,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         if (t >= ks.pt) {
           int u_end;
           bool f;
-          const int u0 = walk.blk_tile(t, u_end, f);
+          const int u0 = at.blk_tile(t, u_end, f);
           if (lane == 0) {
             mbar_arrive_expect_tx(full(st), (uint32_t)prm.box_blk * 128u * C::kHalves);
             for (int hf = 0; hf < C::kHalves; ++hf)
@@ -833,14 +876,16 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       ++gathered;
       return ok;
     };
-    while (ok && walk.next(prm)) {
-      const Keys &ks = walk.ks;
+    for (int it = 0; ok && __all_sync(0xffffffffu, arrive_at(it)); leave(it), ++it) {
+      const Stop<KV4, PAGE> &at = *stop_at(it);
+      const Keys &ks = at.ks;
+      const int nt = at.nt, t0 = at.t0;
       // pages of the tiles j, j + 1, j + 2 of the piece: lane e holds page e
       int lp[3], ph[3];
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         lp[i] = ph[i] = -1;
-        if (i < walk.nt && lane < PPT) walk.page_at(prm, walk.t0 + i, lane, lp[i], ph[i]);
+        if (i < nt && lane < PPT) at.page_at(prm, t0 + i, lane, lp[i], ph[i]);
       }
       auto load = [&](int slot, int phys) {
         const uint32_t dst = base + rawring + slot * C::kRaw;
@@ -860,18 +905,18 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       if (!gather()) break;  // all of the 64 threads have read the piece before
       load(k % 3, ph[0]);
       load((k + 1) % 3, ph[1]);
-      for (int j = 0; j < walk.nt; ++j, ++k) {
-        const int st = k % ST, t = walk.t0 + j;
+      for (int j = 0; j < nt; ++j, ++k) {
+        const int st = k % ST, t = t0 + j;
         const bool blk = t >= ks.pt;
         int lp3 = -1, ph3 = -1;
-        if (j + 3 < walk.nt && lane < PPT) walk.page_at(prm, t + 3, lane, lp3, ph3);
+        if (j + 3 < nt && lane < PPT) at.page_at(prm, t + 3, lane, lp3, ph3);
         cp_async_wait<1>();
         if (!gather()) break;  // everybody's part of tile j is there, and tile j - 1 is read
         load((k + 2) % 3, ph[2]);
         if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (warp == 10) {
-          walk.put_table(prm, table(k), t, lane, lp[0], ph[0]);
+          at.put_table(prm, table(k), t, lane, lp[0], ph[0]);
           __syncwarp();
           if (lane == 0) mbar_arrive(tab_full(k));
         }
@@ -879,7 +924,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           if (tid == 0) {
             int u_end;
             bool f;
-            const int u0 = walk.blk_tile(t, u_end, f);
+            const int u0 = at.blk_tile(t, u_end, f);
             mbar_arrive_expect_tx(full(st), (uint32_t)prm.box_blk * 128u * C::kHalves);
             for (int hf = 0; hf < C::kHalves; ++hf)
               tma_load_3d(base + ring + st * C::kTile + hf * C::kHalf, bmap, full(st), hf * 64, ks.h, ks.s * sh.B + u0);
@@ -1256,23 +1301,23 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
   uint2 *qf = reinterpret_cast<uint2 *>(smem_raw + M::kQ);
   float2 *ml = reinterpret_cast<float2 *>(smem_raw + M::kML);
   float *ow = reinterpret_cast<float *>(smem_raw + M::kO);
-  __shared__ int scan[3], sums[W], more_units;
-  __shared__ Walk<KV4, PAGE> walk;  // the current piece, read where it is needed: registers are short
+  __shared__ int scan[3], sums[W];
+  __shared__ Stop<KV4, PAGE> at;  // the current stop, read where it is needed: registers are short
   const Shape &sh = prm.sh;
   const PagedArgs &a = prm.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   grid_dep_wait();
   grid_dep_launch_dependents();
   cta_share<KV4, PAGE, M::kThreads>(prm, scan, sums);
+  Walk<KV4, PAGE> way(scan);
   if (threadIdx.x == 0) {
-    walk.start(scan);
     if (prm.shared_out) prm.piece[2 * blockIdx.x].unit = prm.piece[2 * blockIdx.x + 1].unit = -1;
   }
   for (;;) {
-    if (threadIdx.x == 0) more_units = walk.next(prm, !prm.shared_out);
+    if (threadIdx.x == 0) way.next(prm, at);
     __syncthreads();
-    if (!more_units) break;
-    const Keys &ks = walk.ks;
+    if (at.nt == 0) break;
+    const Keys &ks = at.ks;
     // queries in the order of the contraction
     for (int e = threadIdx.x; e < NT * (D / 16) * 32; e += M::kThreads) {
       const int ln = e & 31, j = e / 32 % (D / 16), r = 8 * (e / 32 / (D / 16)) + (ln >> 2);
@@ -1301,9 +1346,9 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
       on = 0xffffu;
       hid = 0;
       if (pos != kNever && pos + 16 <= end &&
-          (KV4 || pos + 16 <= walk.first.sk || (pos >= walk.last.lb && pos + 15 <= walk.first.hi)))
+          (KV4 || pos + 16 <= at.first.sk || (pos >= at.last.lb && pos + 15 <= at.first.hi)))
         return;
-      on = visible(pos, 16, end, Limits{walk.first.lb, walk.last.hi, walk.last.sk});
+      on = visible(pos, 16, end, Limits{at.first.lb, at.last.hi, at.last.sk});
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1316,7 +1361,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
     };
     // ---- tiles of pages.  Step i of a warp is 16 keys of tile i / kPerTile; the pages of 32
     //      steps are looked up at a time, a lane each.
-    const int np = max(0, min(walk.nt, ks.pt - walk.t0)) * M::kPerTile, head = ks.h, n_ctx = ks.n;
+    const int np = max(0, min(at.nt, ks.pt - at.t0)) * M::kPerTile, head = ks.h, n_ctx = ks.n;
     auto sub_of = [&](int i) { return warp + W * (i % M::kPerTile); };  // its place in the tile, in 16 keys
     int lps = -1, phs = -1;
     const uint32_t ring = smem_addr(smem_raw) + M::kRing + warp * (M::kSteps * M::Ring::kSlot);
@@ -1326,7 +1371,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
         if ((i & 31) == 0) {
           lps = phs = -1;
           const int e = i + lane;
-          if (e < np) walk.page_at(prm, walk.t0 + e / M::kPerTile, 16 * sub_of(e) / PAGE, lps, phs);
+          if (e < np) at.page_at(prm, at.t0 + e / M::kPerTile, 16 * sub_of(e) / PAGE, lps, phs);
           if (lps != -1 && phs < 0) raise_status(a.status, kStatusBadIndex);
         }
         const int lp = __shfl_sync(0xffffffffu, lps, i & 31), ph = __shfl_sync(0xffffffffu, phs, i & 31);
@@ -1365,10 +1410,10 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
       }
     }
     // ---- tiles of block tokens (bf16)
-    for (int i = np; i < walk.nt * M::kPerTile; ++i) {
+    for (int i = np; i < at.nt * M::kPerTile; ++i) {
       int u_end;
       bool fl;
-      const int u = walk.blk_tile(walk.t0 + i / M::kPerTile, u_end, fl) + 16 * sub_of(i);
+      const int u = at.blk_tile(at.t0 + i / M::kPerTile, u_end, fl) + 16 * sub_of(i);
       if (u >= u_end) continue;
       uint32_t on0, hid0, ph[NT][2], pl[NT][2];
       masks(ks.n + u, ks.n + u_end, on0, hid0);
@@ -1424,9 +1469,9 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
         }
       }
     __syncthreads();
-    const bool whole = walk.begins() && walk.ends();
-    const int slot = 2 * blockIdx.x + (walk.begins() ? 1 : 0);
-    if (!whole && threadIdx.x == 0) prm.piece[slot] = Piece{walk.unit, walk.begins(), walk.ends(), 0};
+    const bool whole = at.begins() && at.ends();
+    const int slot = 2 * blockIdx.x + (at.begins() ? 1 : 0);
+    if (!whole && threadIdx.x == 0) prm.piece[slot] = Piece{at.unit, at.begins(), at.ends(), 0};
     for (int e = threadIdx.x; e < ks.rows * (D / 4); e += M::kThreads) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float mx = -INFINITY, L = 0.f;
