@@ -491,7 +491,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
+    if (elect_one()) {
+      constexpr uint32_t hi = sdesc_hi_sw128(1024);
+      const uint32_t q_lo = sdesc_lo(base + C::kOffQ, 16), k_lo = sdesc_lo(base + C::kOffK, 16),
+                     v_lo = sdesc_lo(base + C::kOffV, C::kHalf);
       constexpr uint32_t ids = idesc_bf16(128, kBN, false, false);
       constexpr uint32_t ido = idesc_bf16(128, D, false, true);
       // S runs two tiles, so up to two stops, ahead of PV: the tile counts of stops between
@@ -517,12 +520,11 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         // P of tile ks - 3 lies in the same columns: its PV must be done
         if (ks >= 3 && !mbar_wait(pv_done(ks - 3), ((ks - 3) >> 1) & 1, ctx)) return false;
         tc_fence_after();
-        const uint32_t sk = base + C::kOffK + st * C::kTile;
+        const uint32_t sk = k_lo + st * (C::kTile >> 4), ds = tmem + (ks % 3) * kBN;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + (ks % 3) * kBN, sdesc_sw128(base + C::kOffQ + at, 16, 1024), sdesc_sw128(sk + at, 16, 1024), ids,
-                    kk > 0 ? 1u : 0u);
+          const uint32_t step = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+          umma_bf16_w(ds, q_lo + step, sk + step, hi, ids, kk > 0 ? 1u : 0u);
         }
         umma_commit(s_full(ks));
         umma_commit(k_empty(st));
@@ -545,11 +547,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           if (ok && j == 0 && it > 0) ok = mbar_wait(o_free, (it - 1) & 1, ctx);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sv = base + C::kOffV + st * C::kTile;
+          const uint32_t sv = v_lo + st * (C::kTile >> 4), pa = tmem + (k % 3) * kBN;
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
-            umma_bf16_ts(tmem + C::kTmemO, tmem + (k % 3) * kBN + kk * 8, sdesc_sw128(sv + kk * 16 * 128, C::kHalf, 1024), ido,
-                         (j > 0 || kk > 0) ? 1u : 0u);
+            umma_bf16_ts_w(tmem + C::kTmemO, pa + kk * 8, sv + kk * (16 * 128 >> 4), hi, ido, (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(pv_done(k));
           umma_commit(v_empty(st));
         }
