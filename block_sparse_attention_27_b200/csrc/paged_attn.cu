@@ -47,6 +47,19 @@ constexpr int kMinTiles = 2;    // least tiles of a share
 constexpr int kManyUnits = 8;   // units per CTA from which shares are whole units
 constexpr int kMaxShared = 1536;  // most units that are cut into equal shares
 
+// A wait in few instructions (these kernels have many, and code that outgrows the
+// instruction cache costs them at every tile): a short spin in place, the bounded wait in
+// a function of its own.
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return mbar_wait(bar, parity, WaitCtx{abort, status});
+}
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, const WaitCtx &ctx) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_long(bar, parity, ctx.abort, ctx.status);
+}
+
 template <int D, bool KV4>
 struct Cfg {
   static constexpr int kHalves = D / 64;
@@ -121,12 +134,21 @@ __device__ __forceinline__ Limits row_limits(const PagedArgs &a, int n, int b) {
                 a.causal ? (int)min((long long)a.sinks, p + 1) : a.sinks};
 }
 
-// Bits j < len whose position base + j is below x.
-__device__ __forceinline__ uint32_t below(int base, int x, int len) {
-  const int c = x <= base ? 0 : min((int)min((long long)x - base, (long long)len), len);
+// Bits j < len whose position base + j (base >= 0) is below x.
+__device__ __forceinline__ uint32_t below(int base, int x, uint32_t len) {
+  const uint32_t c = x <= base ? 0u : min((uint32_t)x - (uint32_t)base, len);
   return c >= 32 ? 0xffffffffu : (1u << c) - 1u;
 }
-__device__ __forceinline__ uint32_t visible(int base, int len, int end, const Limits &w) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Whether one key takes part.
+__device__ __forceinline__ bool seen(int pos, int end, const Limits &w) {
+  return pos < end && (pos < w.sk || (pos >= w.lb && pos <= w.hi));
+}
+__device__ __forceinline__ uint32_t visible(int base, uint32_t len, int end, const Limits &w) {
   if (base == kNever) return 0u;
   return below(base, end, len) & (below(base, w.sk, len) | (~below(base, w.lb, len) & below(base, w.hi + 1, len)));
 }
@@ -298,12 +320,29 @@ __device__ __forceinline__ void cta_share(const Params &prm, int *share, int *su
     const int per = (prm.units + THREADS - 1) / THREADS;  // units of a thread
     const int u0 = threadIdx.x * per, u1 = min(u0 + per, prm.units);
     int mine = 0;
-    auto tiles_of = [&](int u) {
-      Limits x, y;
-      return unit_keys<KV4, PAGE>(prm, u, x, y, blockIdx.x == 0).tiles;
-    };
+    // two rounds over the thread's units: their sum, then (after the scan) the one that the
+    // share begins in
+    int at = 0, lo = 0, hi = 0;
 #pragma unroll 1
-    for (int u = u0; u < u1; ++u) mine += tiles_of(u);
+    for (int round = 0; round < 2; ++round) {
+      const bool look = round == 0 || (lo >= at && lo < at + mine);
+      const int sum0 = mine;
+#pragma unroll 1
+      for (int u = u0; look && u < u1; ++u) {
+        Limits x, y;
+        const int n = round == 1 && per == 1 ? sum0 : unit_keys<KV4, PAGE>(prm, u, x, y, blockIdx.x == 0).tiles;
+        if (round == 0) {
+          mine += n;
+        } else {
+          if (lo >= at && lo < at + n) {
+            share[0] = u;
+            share[1] = lo - at;
+            share[2] = hi - lo;
+          }
+          at += n;
+        }
+      }
+      if (round == 1) break;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -317,23 +356,10 @@ __device__ __forceinline__ void cta_share(const Params &prm, int *share, int *su
       before += w < warp ? sums[w] : 0;
       total += sums[w];
     }
-    const int shares = max(1, min((int)gridDim.x, total / kMinTiles));
-    const int c = blockIdx.x;
-    if (c < shares) {
-      const int lo = (int)((long long)total * c / shares), hi = (int)((long long)total * (c + 1) / shares);
-      int at = before + upto - mine;  // first tile of this thread's units
-      if (lo >= at && lo < at + mine) {
-#pragma unroll 1
-        for (int u = u0; u < u1; ++u) {
-          const int n = per == 1 ? mine : tiles_of(u);
-          if (lo >= at && lo < at + n) {
-            share[0] = u;
-            share[1] = lo - at;
-            share[2] = hi - lo;
-          }
-          at += n;
-        }
-      }
+    const int shares = max(1, min((int)gridDim.x, total / kMinTiles)), c = blockIdx.x;
+    at = before + upto - mine;  // first tile of this thread's units
+    lo = c < shares ? (int)((long long)total * c / shares) : INT_MAX;
+    hi = c < shares ? (int)((long long)total * (c + 1) / shares) : INT_MAX;
     }
   }
   __syncthreads();
@@ -394,12 +420,14 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   const int aw = (prm.bpt * sh.G + 31) / 32;  // warps of a group that hold rows; the others rest
 
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int st = 0; st < ST; ++st) {
       mbar_init(k_full(st), kLoaders);
       mbar_init(k_empty(st), 1);
       mbar_init(v_full(st), kLoaders);
       mbar_init(v_empty(st), 1);
     }
+#pragma unroll 1
     for (int k = 0; k < kTabs; ++k) mbar_init(tab_full(k), 1);
     for (int k = 0; k < 3; ++k) {
       mbar_init(s_full(k), 1);
@@ -440,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   // The role's next stop: waits for it, and (done) gives the last one's slot back.  False at
   // the end of the walk, and where a wait gave up.
   auto arrive_at = [&](int it) {
-    return mbar_wait(stop_full(it), (it / 3) & 1, ctx) && stop_at(it)->nt > 0;
+    return mbar_wait_short(stop_full(it), (it / 3) & 1, ctx) && stop_at(it)->nt > 0;
   };
   auto leave = [&](int it) {
     __syncwarp();
@@ -475,18 +503,18 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       Walk<KV4, PAGE> walk(scan);
       int loaded = 0;
       for (int it = 0;; ++it) {
-        if (it >= 3 && !mbar_wait(stop_empty(it), ((it / 3) - 1) & 1, ctx)) break;
+        if (it >= 3 && !mbar_wait_short(stop_empty(it), ((it / 3) - 1) & 1, ctx)) break;
         Stop<KV4, PAGE> &at = *stop_at(it);
         const bool more = walk.next(prm, at);
         mbar_arrive(stop_full(it));
         if (!more) break;
-        if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, ctx)) break;
+        if (it > 0 && !mbar_wait_short(q_empty, (it - 1) & 1, ctx)) break;
         mbar_arrive_expect_tx(q_full, (uint32_t)prm.bpt * sh.G * 128u * C::kHalves);
         for (int hf = 0; hf < C::kHalves; ++hf)
           tma_load_3d(base + C::kOffQ + hf * C::kHalf, &qmap, q_full, hf * 64, at.ks.h * sh.G, at.ks.s * sh.B + at.ks.b0);
         loaded = it + 1;
       }
-      if (loaded > 0) mbar_wait(q_full, (loaded - 1) & 1, drain_ctx);  // a copy in flight lands before the CTA ends
+      if (loaded > 0) mbar_wait_short(q_full, (loaded - 1) & 1, drain_ctx);  // a copy in flight lands before the CTA ends
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -504,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       auto issue_s = [&]() {
         if (s_left == 0) {
           if (!more) return true;
-          if (!mbar_wait(stop_full(s_it), (s_it / 3) & 1, ctx)) return false;
+          if (!mbar_wait_short(stop_full(s_it), (s_it / 3) & 1, ctx)) return false;
           s_left = stop_at(s_it)->nt;
           mbar_arrive(stop_empty(s_it));
 #pragma unroll
@@ -512,13 +540,13 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             if (i == (s_it & 3)) counts[i] = s_left;
           more = s_left > 0;
           if (!more) return true;
-          if (!mbar_wait(q_full, s_it & 1, ctx)) return false;
+          if (!mbar_wait_short(q_full, s_it & 1, ctx)) return false;
           ++s_it;
         }
         const int st = ks % ST;
-        if (!mbar_wait(k_full(st), (ks / ST) & 1, ctx)) return false;
+        if (!mbar_wait_short(k_full(st), (ks / ST) & 1, ctx)) return false;
         // P of tile ks - 3 lies in the same columns: its PV must be done
-        if (ks >= 3 && !mbar_wait(pv_done(ks - 3), ((ks - 3) >> 1) & 1, ctx)) return false;
+        if (ks >= 3 && !mbar_wait_short(pv_done(ks - 3), ((ks - 3) >> 1) & 1, ctx)) return false;
         tc_fence_after();
         const uint32_t sk = k_lo + st * (C::kTile >> 4), ds = tmem + (ks % 3) * kBN;
 #pragma unroll
@@ -542,9 +570,9 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         if (it >= s_it || nt == 0) break;
         for (int j = 0; ok && j < nt; ++j, ++k) {
           const int st = k % ST;
-          ok = issue_s() && mbar_wait(p_full(k), (k / 3) & 1, ctx) && mbar_wait(v_full(st), (k / ST) & 1, ctx);
+          ok = issue_s() && mbar_wait_short(p_full(k), (k / 3) & 1, ctx) && mbar_wait_short(v_full(st), (k / ST) & 1, ctx);
           // the epilogue of the unit before has read O
-          if (ok && j == 0 && it > 0) ok = mbar_wait(o_free, (it - 1) & 1, ctx);
+          if (ok && j == 0 && it > 0) ok = mbar_wait_short(o_free, (it - 1) & 1, ctx);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sv = v_lo + st * (C::kTile >> 4), pa = tmem + (k % 3) * kBN;
@@ -557,7 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         if (ok) umma_commit(o_full);
       }
       umma_commit(drain);  // every issued MMA completes before TMEM and the tiles are released
-      mbar_wait(drain, 0, drain_ctx);
+      mbar_wait_short(drain, 0, drain_ctx);
     }
     __syncwarp();
   } else if (warp >= 2 && warp < 10) {
@@ -571,7 +599,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       // all softmax threads; a bounded wait, unlike a named barrier
       auto meet_all = [&]() {
         mbar_arrive(meet);
-        alive = __all_sync(0xffffffffu, mbar_wait(meet, met & 1, ctx));
+        alive = __all_sync(0xffffffffu, mbar_wait_short(meet, met & 1, ctx));
         ++met;
         return alive;
       };
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         const int k1 = k0 + at.nt;
         for (int k = k0 + ((k0 ^ g) & 1); k < k1; k += 2) {
           const uint32_t sc = lt + (k % 3) * kBN;
-          alive = __all_sync(0xffffffffu, mbar_wait(tab_full(k), (k / kTabs) & 1, ctx) && mbar_wait(s_full(k), (k / 3) & 1, ctx));
+          alive = __all_sync(0xffffffffu, mbar_wait_short(tab_full(k), (k / kTabs) & 1, ctx) && mbar_wait_short(s_full(k), (k / 3) & 1, ctx));
           if (!alive) break;
           tc_fence_after();
           const int *tab = table(k);
@@ -601,11 +629,12 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w) bits[w] = visible32<PAGE>(tab, blk, w, end, mine);
             // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
-            alive = __all_sync(0xffffffffu, mbar_wait(v_full(st), (k / ST) & 1, ctx));
+            alive = __all_sync(0xffffffffu, mbar_wait_short(v_full(st), (k / ST) & 1, ctx));
             if (!alive) break;
+#pragma unroll 1
             for (int key = quarter * 32 + lane; key < kBN; key += 32 * aw) {
-              const uint32_t any = visible32<PAGE>(tab, blk, key >> 5, end, all);
-              if ((any >> (key & 31)) & 1u) continue;
+              const int from = blk ? tab[0] : tab[key / PAGE];
+              if (from != kNever && seen(from + (blk ? key : key % PAGE), end, all)) continue;
               unsigned char *row = smem + C::kOffV + st * C::kTile + key * 128;
 #pragma unroll
               for (int hf = 0; hf < C::kHalves; ++hf)
@@ -633,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
 #pragma unroll
           for (int w = 0; w < kHold / 32; ++w) hide(x + 32 * w, w);
 #pragma unroll
-          for (int j = 0; j < kHold; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+          for (int j = 0; j < kHold; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
           if constexpr (KV4) {
 #pragma unroll
             for (int w = 2; w < 4; ++w) {
@@ -641,25 +670,25 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
               tmem_ld32(sc + 32 * w, y);
               hide(y, w);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(y[j]));
+              for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
             }
           }
           const float tmax = r < rows ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sh.sl2 : -INFINITY;
           // the reference so far, from the group of the tile before; a row past the unit's keeps none
           float m_prev = -INFINITY;
           if (k > k0) {
-            alive = __all_sync(0xffffffffu, mbar_wait(decided(k - 1), ((k - 1) >> 1) & 1, ctx));
+            alive = __all_sync(0xffffffffu, mbar_wait_short(decided(k - 1), ((k - 1) >> 1) & 1, ctx));
             if (!alive) break;
             m_prev = m_ref[r];
           }
           const bool need = tmax > m_prev + kRescaleLog2 || (m_prev == -INFINITY && tmax > -INFINITY);
           const float m_now = need ? tmax : m_prev;
           if (k > k0 && __any_sync(0xffffffffu, need)) {  // O holds the unit's earlier tiles
-            alive = __all_sync(0xffffffffu, mbar_wait(pv_done(k - 1), ((k - 1) >> 1) & 1, ctx));
+            alive = __all_sync(0xffffffffu, mbar_wait_short(pv_done(k - 1), ((k - 1) >> 1) & 1, ctx));
             if (!alive) break;
             tc_fence_after();
             const float alpha = !need ? 1.f : m_prev == -INFINITY ? 0.f : fast_exp2(m_prev - m_now);
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o[32];
               tmem_ld32(oc + c0, o);
@@ -707,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         if (!alive) break;
         // ---- the unit's rows: both groups' sums on the common reference, O from TMEM, a
         //      group per half of the columns
-        alive = __all_sync(0xffffffffu, mbar_wait(o_full, it & 1, ctx));
+        alive = __all_sync(0xffffffffu, mbar_wait_short(o_full, it & 1, ctx));
         if (!alive) break;
         tc_fence_after();
         if (!meet_all()) break;  // m_ref is final
@@ -733,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           }
         }
         if (!whole && warp == 4 && lane == 0) prm.piece[slot] = Piece{at.unit, at.begins(), at.ends(), 0};
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < D / 2; i0 += 32) {
           const int c0 = g * (D / 2) + i0;
           uint32_t o[32];
@@ -779,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         const int st = k % ST, t = t0 + j;
         int lp1 = -1, phys1 = -1;  // the next tile's pages, fetched before this tile's wait
         if (j + 1 < nt && lane < PPT) at.page_at(prm, t + 1, lane, lp1, phys1);
-        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
+        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait_short(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (!isv) {
           at.put_table(prm, table(k), t, lane, lp, phys);
@@ -814,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           constexpr int LPR = D / 8;
           const int cr = lane % LPR, row0 = lane / LPR;
           const uint32_t dcol = (cr >> 3) * C::kHalf;
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < PPT; ++e) {
             const int ph = __shfl_sync(0xffffffffu, phys, e);
             if (ph < 0) continue;
@@ -850,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     }
     // copies in flight land before the CTA's shared memory is released
     if (lane == 0)
-      for (int j = max(0, k - ST); j < k; ++j) mbar_wait(full(j % ST), (j / ST) & 1, drain_ctx);
+      for (int j = max(0, k - ST); j < k; ++j) mbar_wait_short(full(j % ST), (j / ST) & 1, drain_ctx);
     __syncwarp();
   } else {
     // ------------------------------------------- 4-bit rows into bf16 tiles --
@@ -873,7 +902,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     bool ok = true;
     auto gather = [&]() {  // the 64 threads; a bounded wait, unlike a named barrier
       mbar_arrive(loaders(isv));
-      ok = __all_sync(0xffffffffu, mbar_wait(loaders(isv), gathered & 1, ctx));
+      ok = __all_sync(0xffffffffu, mbar_wait_short(loaders(isv), gathered & 1, ctx));
       ++gathered;
       return ok;
     };
@@ -890,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       }
       auto load = [&](int slot, int phys) {
         const uint32_t dst = base + rawring + slot * C::kRaw;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < CH; ++i) {
           const int c = tid + 64 * i, key = c / GR;
           const int p = __shfl_sync(0xffffffffu, phys, key / PAGE);
@@ -914,7 +943,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         cp_async_wait<1>();
         if (!gather()) break;  // everybody's part of tile j is there, and tile j - 1 is read
         load((k + 2) % 3, ph[2]);
-        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((k / ST) - 1) & 1, ctx));
+        if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait_short(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
         if (warp == 10) {
           at.put_table(prm, table(k), t, lane, lp[0], ph[0]);
@@ -935,7 +964,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         } else {
           const unsigned char *src = smem + rawring + (k % 3) * C::kRaw;
           unsigned char *dst = smem + ring + st * C::kTile;
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < CH; ++i) {
             const int c = tid + 64 * i, key = c / GR, grp = c % GR;
             const int p = __shfl_sync(0xffffffffu, ph[0], key / PAGE), q = __shfl_sync(0xffffffffu, lp[0], key / PAGE);
@@ -965,7 +994,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
       cp_async_wait<0>();
     }
     if (tid == 0)  // copies in flight land before the CTA's shared memory is released
-      for (int j = max(0, k - ST); j < k; ++j) mbar_wait(full(j % ST), (j / ST) & 1, drain_ctx);
+      for (int j = max(0, k - ST); j < k; ++j) mbar_wait_short(full(j % ST), (j / ST) & 1, drain_ctx);
     __syncwarp();
   }
 
@@ -1280,8 +1309,10 @@ __device__ __forceinline__ void few_values(F &f, FewState<D, NT> &st, const uint
 template <int D, bool KV4, int NT>
 struct FewCfg {
   using Ring = typename std::conditional<KV4, RingKv4<D>, RingBf16<D>>::type;
-  // two CTAs an SM.  The bf16 cache needs bytes in flight (8 warps x 3 steps of 8 KB an SM),
-  // the 4-bit one warps to unpack (16, 4 steps of 2.3 KB each)
+  // Two CTAs an SM.  The bf16 cache needs bytes in flight (8 warps x 3 steps of 8 KB an SM),
+  // the 4-bit one warps to unpack (16, 4 steps of 2.3 KB each); with 16 rows these want more
+  // registers than two CTAs leave.
+  static constexpr int kPerSm = KV4 && NT == 2 ? 1 : 2;
   static constexpr int kWarps = KV4 ? 8 : 4, kSteps = KV4 ? 4 : 3;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPerTile = 8 / kWarps;                          // steps of a warp per tile
@@ -1295,7 +1326,7 @@ struct FewCfg {
 };
 
 template <int D, int PAGE, bool KV4, int NT>
-__global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, FewCfg<D, KV4, NT>::kPerSm) paged_few(const __grid_constant__ Params prm) {
   using M = FewCfg<D, KV4, NT>;
   constexpr int W = M::kWarps;
   extern __shared__ unsigned char smem_raw[];
@@ -1366,8 +1397,8 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
     auto sub_of = [&](int i) { return warp + W * (i % M::kPerTile); };  // its place in the tile, in 16 keys
     int lps = -1, phs = -1;
     const uint32_t ring = smem_addr(smem_raw) + M::kRing + warp * (M::kSteps * M::Ring::kSlot);
-    int pos[M::kSteps];  // position of the step's first key
-    auto issue = [&](int slot, int i) {
+    int pos_of = kNever;  // position of the first key of the step i with i % 32 = lane
+    auto issue = [&](int i) {
       if (i < np) {
         if ((i & 31) == 0) {
           lps = phs = -1;
@@ -1377,38 +1408,35 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, 2) paged_few(con
         }
         const int lp = __shfl_sync(0xffffffffu, lps, i & 31), ph = __shfl_sync(0xffffffffu, phs, i & 31);
         const int in_page = 16 * sub_of(i) % PAGE;
-        pos[slot] = ph >= 0 ? lp * PAGE + in_page : kNever;
-        if (ph >= 0 && pos[slot] < n_ctx)
-          M::Ring::fetch(ring + slot * M::Ring::kSlot, a, ((long long)ph * sh.Hkv + head) * PAGE + in_page, lane);
+        const int pos = ph >= 0 ? lp * PAGE + in_page : kNever;
+        if (lane == (i & 31)) pos_of = pos;
+        if (ph >= 0 && pos < n_ctx)
+          M::Ring::fetch(ring + i % M::kSteps * M::Ring::kSlot, a, ((long long)ph * sh.Hkv + head) * PAGE + in_page, lane);
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int d = 0; d < M::kSteps; ++d) issue(d, d);
-    for (int i0 = 0; i0 < np; i0 += M::kSteps) {
-#pragma unroll
-      for (int d = 0; d < M::kSteps; ++d) {
-        if (i0 + d < np) {
-          uint32_t on, hid;
-          masks(pos[d], n_ctx, on, hid);
-          cp_async_wait<M::kSteps - 1>();
-          __syncwarp();  // every lane's part of the step is there
-          if (on) {      // the same in every lane
-            float x[NT][4];
-            uint32_t ph[NT][2], pl[NT][2];
-            typename M::Ring f;
-            f.at = smem_raw + M::kRing + (warp * M::kSteps + d) * M::Ring::kSlot;
-            f.g = g;
-            f.t = t4;
-            few_scores<D, NT>(f, qf, lane, x);
-            f.v_begin(on);
-            few_softmax<D, NT>(st, x, hid, sh.sl2, ph, pl);
-            few_values<D, NT>(f, st, ph, pl);
-          }
-          __syncwarp();  // every lane has read the slot
-          issue(d, i0 + d + M::kSteps);
-        }
+#pragma unroll 1
+    for (int i = 0; i < M::kSteps; ++i) issue(i);
+#pragma unroll 1
+    for (int i = 0; i < np; ++i) {
+      uint32_t on, hid;
+      masks(__shfl_sync(0xffffffffu, pos_of, i & 31), n_ctx, on, hid);
+      cp_async_wait<M::kSteps - 1>();
+      __syncwarp();  // every lane's part of the step is there
+      if (on) {      // the same in every lane
+        float x[NT][4];
+        uint32_t ph[NT][2], pl[NT][2];
+        typename M::Ring f;
+        f.at = smem_raw + M::kRing + (warp * M::kSteps + i % M::kSteps) * M::Ring::kSlot;
+        f.g = g;
+        f.t = t4;
+        few_scores<D, NT>(f, qf, lane, x);
+        f.v_begin(on);
+        few_softmax<D, NT>(st, x, hid, sh.sl2, ph, pl);
+        few_values<D, NT>(f, st, ph, pl);
       }
+      __syncwarp();  // every lane has read the slot
+      issue(i + M::kSteps);
     }
     // ---- tiles of block tokens (bf16)
     for (int i = np; i < at.nt * M::kPerTile; ++i) {
@@ -1582,11 +1610,13 @@ Geometry geometry(const Shape &sh) {
   return g;
 }
 
-PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles) {
+PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles, bool kv4) {
   const Geometry g = geometry(sh);
   PagedPlan p{};
   p.few = g.rows <= kFewRows;
-  const int ctas = p.few ? 2 * sms : sms;
+  const int per_sm = !p.few ? 1 : kv4 ? (g.rows <= 8 ? FewCfg<128, true, 1>::kPerSm : FewCfg<128, true, 2>::kPerSm)
+                                      : FewCfg<128, false, 1>::kPerSm;
+  const int ctas = per_sm * sms;
   // whole units where there are many, or where none is long enough to be cut
   p.shared_out = g.units <= std::min((long long)kManyUnits * ctas, (long long)kMaxShared) && max_tiles > kMinTiles;
   p.ctas = p.shared_out ? ctas : (int)std::min<long long>(ctas, g.units);
@@ -1667,12 +1697,12 @@ PagedPlan plan_window(const Shape &sh, int num_sms, int window, int sinks) {
   const Geometry g = geometry(sh);
   const long long prefix = (long long)sh.max_pages * sh.P;
   const long long reach = std::min(prefix, (long long)window + sinks) + std::min((long long)sh.B, (long long)window + g.bpt);
-  return make_plan(sh, num_sms, (reach + kBN - 1) / kBN);
+  return make_plan(sh, num_sms, (reach + kBN - 1) / kBN, false);
 }
 
 PagedPlan plan_kv4(const Shape &sh, int num_sms, bool sparse) {
   const long long prefix = (long long)(sparse ? std::min(sh.kmax, sh.max_pages) : sh.max_pages) * sh.P;
-  return make_plan(sh, num_sms, (prefix + kBN - 1) / kBN + (sh.B + kBN - 1) / kBN);
+  return make_plan(sh, num_sms, (prefix + kBN - 1) / kBN + (sh.B + kBN - 1) / kBN, true);
 }
 
 cudaError_t launch_window(const Shape &sh, const PagedPlan &plan, const PagedArgs &a, cudaStream_t stream) {
