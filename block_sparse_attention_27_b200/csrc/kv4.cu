@@ -16,117 +16,170 @@ __device__ __forceinline__ float kv4_scale(float amax) {
   return __uint_as_float((__float_as_uint(__fdiv_rn(amax, 7.f)) + 0x7ffffu) & ~0x7ffffu);
 }
 
-template <int D>
+// Walks a CTA's rows (token, K | V, head), kRows apart: TT tokens from t0, found once per
+// token and kept in shared memory (looked up by every lane, they were most of the
+// instructions that bound these kernels: 284 and 165 a lane and row).
+template <int D, int TT>
+struct Rows {
+  static constexpr int kLanes = D / 8, kPass = kKv4Threads / kLanes;
+  int i, r, n, di, dr;  // token of the CTA, row of it, rows of a token; the step of one pass
+  __device__ __forceinline__ Rows(int n_) : n(n_) {
+    const int row = threadIdx.x / kLanes;
+    i = row / n;
+    r = row - i * n;
+    di = kPass / n;
+    dr = kPass - di * n;
+  }
+  __device__ __forceinline__ void step() {
+    i += di;
+    r += dr;
+    if (r >= n) {
+      r -= n;
+      ++i;
+    }
+  }
+};
+// Row of head 0 in the cache of each of the CTA's tokens (head h is h * P further), -1: none.
+template <int TT>
+__device__ __forceinline__ void find_tokens(const Shape &sh, long long t0, const int32_t *__restrict__ first,
+                                            const int32_t *__restrict__ n_new, uint32_t *status, long long (&rows)[TT]) {
+  if (threadIdx.x < TT) {
+    const long long t = t0 + threadIdx.x;
+    long long row = -1;
+    if (t < (long long)sh.S * sh.B) {
+      const int s = (int)((unsigned)t / (unsigned)sh.B), b = (int)(t - (long long)s * sh.B);
+      if (b < block_tokens(n_new, s, sh.B, status, b == 0)) {
+        const int n = first[s];
+        const long long at = (long long)n + b;
+        const long long phys = n < 0 ? -1 : physical_page(sh, s, at / sh.P);
+        if (phys < 0)
+          raise_status(status, kStatusBadIndex);
+        else
+          row = phys * sh.Hkv * sh.P + at % sh.P;
+      }
+    }
+    rows[threadIdx.x] = row;
+  }
+  __syncthreads();
+}
+
+template <int D, int TT>
 __global__ void __launch_bounds__(kKv4Threads)
     kv4_store(const Shape sh, const Kv4 c, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
               const int32_t *__restrict__ n_ctx, const int32_t *__restrict__ n_new, uint32_t *status) {
-  constexpr int kLanes = D / 8;
+  __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
-  const long long item = (long long)blockIdx.x * (kKv4Threads / kLanes) + threadIdx.x / kLanes;  // (token, k|v, head)
-  const int l = threadIdx.x % kLanes;
-  const long long t = item / (2 * sh.Hkv);
-  const int r = (int)(item % (2 * sh.Hkv));
-  const bool isv = r >= sh.Hkv;
-  const int h = isv ? r - sh.Hkv : r;
-  bool on = t < (long long)sh.S * sh.B;
-  long long row = 0;
-  if (on) {
-    const int s = (int)(t / sh.B), b = (int)(t % sh.B);
-    on = b < block_tokens(n_new, s, sh.B, status, b == 0 && r == 0 && l == 0);
-    if (on) {
-      const int n = n_ctx[s];
-      const long long phys = n < 0 ? -1 : physical_page(sh, s, ((long long)n + b) / sh.P);
-      if (phys < 0) {
-        if (r == 0 && l == 0) raise_status(status, kStatusBadIndex);
-        on = false;
-      } else {
-        row = (phys * sh.Hkv + h) * sh.P + (n + b) % sh.P;
+  const long long t0 = (long long)blockIdx.x * TT;
+  find_tokens<TT>(sh, t0, n_ctx, n_new, status, rows);
+  Rows<D, TT> at(2 * sh.Hkv);
+  const int l = threadIdx.x % Rows<D, TT>::kLanes;
+  uint4 next = make_uint4(0, 0, 0, 0);
+  auto load = [&]() {
+    next = make_uint4(0, 0, 0, 0);
+    if (at.i >= TT || rows[at.i] < 0) return;
+    const bool isv = at.r >= sh.Hkv;
+    next = __ldg(reinterpret_cast<const uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + (isv ? at.r - sh.Hkv : at.r)) * D) + l);
+  };
+  load();
+  // whole warps go round: a group's maximum is a shuffle
+#pragma unroll 1
+  for (int done = 0; done < TT * 2 * sh.Hkv; done += Rows<D, TT>::kPass) {
+    const uint4 raw = next;
+    const int i = at.i, r = at.r;
+    at.step();
+    load();
+    float x[8];
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(p[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+    float amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = fmaxf(amax, fabsf(x[i]));
+      bad |= x[i] != x[i];
+    }
+    if (bad) amax = INFINITY;  // fmaxf drops NaN
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float s = kv4_scale(amax);
+    uint32_t w = 0x88888888u;
+    if (s > 0.f) {
+      // Nearest integer to x / s, ties to even, without a division each.  2 x / s differs from
+      // an integer m >= 1 by nothing or by at least 2^-8 (x has eight significant bits, s five,
+      // x <= 7 s), so a product within 2^-10 of m stands for m itself, and a half-way quotient
+      // is met exactly.  The sum with 1.5 * 2^23 + 8 rounds to an integer, ties to even, and
+      // leaves the code in the low bits.
+      const float inv = __fdiv_rn(2.f, s);
+      constexpr float kMagic = 12582912.f;
+      w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = x[i] * inv, m = __fadd_rn(__fadd_rn(y, kMagic), -kMagic);
+        const float z = fabsf(y - m) < 0.0009765625f ? m : y;
+        w |= (__float_as_uint(__fmaf_rn(z, 0.5f, kMagic + 8.f)) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
       }
     }
+    if (i >= TT || rows[i] < 0) continue;
+    const bool isv = r >= sh.Hkv;
+    const long long row = rows[i] + (isv ? r - sh.Hkv : r) * sh.P;
+    *reinterpret_cast<uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l) = w;
+    if (l % 4 == 0) (isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4] = __float2bfloat16_rn(s);
   }
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (on) raw = *reinterpret_cast<const uint4 *>((isv ? v : k) + (t * sh.Hkv + h) * D + 8 * l);
-  float x[8];
-  const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&raw);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(p[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-  float amax = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    bad |= x[i] != x[i];
-  }
-  if (bad) amax = INFINITY;  // fmaxf drops NaN
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const float s = kv4_scale(amax);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q = 8.f;
-    if (s > 0.f) q += fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f);
-    w |= (uint32_t)q << (4 * (i >> 1) + 16 * (i & 1));
-  }
-  if (!on) return;
-  *reinterpret_cast<uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l) = w;
-  if (l % 4 == 0) (isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4] = __float2bfloat16_rn(s);
 }
 
-template <int D>
+template <int D, int TT>
 __global__ void __launch_bounds__(kKv4Threads)
     kv4_load(const Shape sh, const Kv4 c, __nv_bfloat16 *__restrict__ k, __nv_bfloat16 *__restrict__ v,
              const int32_t *__restrict__ start, const int32_t *__restrict__ n_new, uint32_t *status) {
-  constexpr int kLanes = D / 8;
+  __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
-  const long long item = (long long)blockIdx.x * (kKv4Threads / kLanes) + threadIdx.x / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const long long t = item / (2 * sh.Hkv);
-  const int r = (int)(item % (2 * sh.Hkv));
-  const bool isv = r >= sh.Hkv;
-  const int h = isv ? r - sh.Hkv : r;
-  if (t >= (long long)sh.S * sh.B) return;
-  const int s = (int)(t / sh.B), b = (int)(t % sh.B);
-  const bool lead = r == 0 && l == 0;
-  if (b >= block_tokens(n_new, s, sh.B, status, lead && b == 0)) return;
-  const int n = start[s];
-  const long long phys = n < 0 ? -1 : physical_page(sh, s, ((long long)n + b) / sh.P);
-  if (phys < 0) {
-    if (lead) raise_status(status, kStatusBadIndex);
-    return;
+  const long long t0 = (long long)blockIdx.x * TT;
+  find_tokens<TT>(sh, t0, start, n_new, status, rows);
+  Rows<D, TT> at(2 * sh.Hkv);
+  const int l = threadIdx.x % Rows<D, TT>::kLanes;
+#pragma unroll 4
+  for (; at.i < TT; at.step()) {
+    if (rows[at.i] < 0) continue;
+    const bool isv = at.r >= sh.Hkv;
+    const int h = isv ? at.r - sh.Hkv : at.r;
+    const long long row = rows[at.i] + h * sh.P;
+    const uint32_t w = *reinterpret_cast<const uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l);
+    __nv_bfloat162 s8, m24;
+    kv4_constants((isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4], s8, m24);
+    *reinterpret_cast<uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + h) * D + 8 * l) =
+        make_uint4(kv4_pair(w, 0, s8, m24), kv4_pair(w, 1, s8, m24), kv4_pair(w, 2, s8, m24), kv4_pair(w, 3, s8, m24));
   }
-  const long long row = (phys * sh.Hkv + h) * sh.P + (n + b) % sh.P;
-  const uint32_t w = *reinterpret_cast<const uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l);
-  __nv_bfloat162 s8, m24;
-  kv4_constants((isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4], s8, m24);
-  *reinterpret_cast<uint4 *>((isv ? v : k) + (t * sh.Hkv + h) * D + 8 * l) =
-      make_uint4(kv4_pair(w, 0, s8, m24), kv4_pair(w, 1, s8, m24), kv4_pair(w, 2, s8, m24), kv4_pair(w, 3, s8, m24));
 }
 
-template <int D>
-unsigned rows_grid(const Shape &sh) {
-  constexpr int kRows = kKv4Threads / (D / 8);
-  return (unsigned)(((long long)sh.S * sh.B * 2 * sh.Hkv + kRows - 1) / kRows);
-}
+unsigned tokens_grid(const Shape &sh, int per) { return (unsigned)(((long long)sh.S * sh.B + per - 1) / per); }
+// Sixteen tokens a CTA once they still give every SM four CTAs, else one.
+constexpr int kTokens = 16;
+bool many_tokens(const Shape &sh) { return tokens_grid(sh, kTokens) >= 4u * 148u; }
 
 }  // namespace
 
+#define DSA_KV4_LAUNCH(kern, ...)                                                                                      \
+  if (many_tokens(sh))                                                                                                 \
+    return sh.d == 128 ? launch_pdl(kern<128, kTokens>, dim3(tokens_grid(sh, kTokens)), kKv4Threads, 0, stream, __VA_ARGS__) \
+                       : launch_pdl(kern<64, kTokens>, dim3(tokens_grid(sh, kTokens)), kKv4Threads, 0, stream, __VA_ARGS__); \
+  return sh.d == 128 ? launch_pdl(kern<128, 1>, dim3(tokens_grid(sh, 1)), kKv4Threads, 0, stream, __VA_ARGS__)          \
+                     : launch_pdl(kern<64, 1>, dim3(tokens_grid(sh, 1)), kKv4Threads, 0, stream, __VA_ARGS__)
+
 cudaError_t launch_kv4_store(const Shape &sh, const Kv4 &c, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
                              const int32_t *n_ctx, const int32_t *n_new, uint32_t *status, cudaStream_t stream) {
-  return sh.d == 128 ? launch_pdl(kv4_store<128>, dim3(rows_grid<128>(sh)), kKv4Threads, 0, stream, sh, c, k, v, n_ctx, n_new, status)
-                     : launch_pdl(kv4_store<64>, dim3(rows_grid<64>(sh)), kKv4Threads, 0, stream, sh, c, k, v, n_ctx, n_new, status);
+  DSA_KV4_LAUNCH(kv4_store, sh, c, k, v, n_ctx, n_new, status);
 }
 
 cudaError_t launch_kv4_load(const Shape &sh, const Kv4 &c, __nv_bfloat16 *k, __nv_bfloat16 *v, const int32_t *start,
                             const int32_t *n_new, uint32_t *status, cudaStream_t stream) {
-  return sh.d == 128 ? launch_pdl(kv4_load<128>, dim3(rows_grid<128>(sh)), kKv4Threads, 0, stream, sh, c, k, v, start, n_new, status)
-                     : launch_pdl(kv4_load<64>, dim3(rows_grid<64>(sh)), kKv4Threads, 0, stream, sh, c, k, v, start, n_new, status);
+  DSA_KV4_LAUNCH(kv4_load, sh, c, k, v, start, n_new, status);
 }
 
 }  // namespace dsa

@@ -43,7 +43,7 @@ constexpr int kRowsPerTile = 128;
 constexpr int kNever = INT_MAX;  // position of a key that takes no part
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kTabs = 8;        // tiles whose positions are kept: six are in flight at most
-constexpr int kMinTiles = 2;    // least tiles of a share
+constexpr int kMinTiles = 1;    // least tiles of a share
 constexpr int kManyUnits = 8;   // units per CTA from which shares are whole units
 constexpr int kMaxShared = 1536;  // most units that are cut into equal shares
 
@@ -626,8 +626,13 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             const int end = tab[9], st = k % ST;
             const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
             const Limits all{at.first.lb, at.last.hi, at.last.sk};  // keys that some row may see
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t b = visible32<PAGE>(tab, blk, w, end, mine);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) bits[w] = visible32<PAGE>(tab, blk, w, end, mine);
+              for (int i = 0; i < 4; ++i)
+                if (i == w) bits[i] = b;
+            }
             // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
             alive = __all_sync(0xffffffffu, mbar_wait_short(v_full(st), (k / ST) & 1, ctx));
             if (!alive) break;

@@ -346,32 +346,42 @@ def dsa_merge_attn(o_a, lse_a, o_b, lse_b, o_out, lse_out=None, stream=None):
 
 
 # ------------------------------------------- operators beside the two passes ----
-def _arg(t, name, dtype, shape=None):
-    """Address of a contiguous CUDA tensor on the current device, checked; None stays None
-    only where the caller allows it (it does not call this then)."""
+# A call's host time counts where its kernel takes a few microseconds: each tensor is checked
+# in one expression, and the reason is worked out only where that fails.
+def _refuse(t, name, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, name, dtype, shape=None, dev=None):
+    """Address of a contiguous tensor of that type and shape on the current device."""
+    if dev is None:
+        dev = torch.cuda.current_device()
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev
+            or (shape is not None and t.shape != shape) or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _opt(t, name, dtype, shape=None):
-    return None if t is None else _arg(t, name, dtype, shape)
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _ws(workspace):
-    return _arg(workspace.buf, "workspace", torch.uint8)
+def _ws(workspace, dev):
+    buf = workspace.buf
+    return _arg(buf, "workspace", torch.uint8, None, dev)
 
 
-def _raw_stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+def _raw_stream(stream, dev):
+    # (torch.cuda.current_stream() builds a Stream object, which takes as long as the call itself)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _call(rc, what):
@@ -434,22 +444,20 @@ class Rope:
                 _arg(w, name, torch.bfloat16)
                 if w.dim() != 1:
                     raise ValueError(f"{name} must have one dimension")
+        self.device = inv_freq.get_device()
+        self.c = dsa_rope(self.rot, self.interleaved, self.eps, self.scale, inv_freq.data_ptr(), None,
+                          None if q_norm is None else q_norm.data_ptr(),
+                          None if k_norm is None else k_norm.data_ptr())
 
 
-def _projection(t, name, dims, H):
+def _projection(t, name, S, B, H, d, dev):
     """Address and token stride of a projection [S, B, H, d] whose tokens may be a view into a
     packed row."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (dims.S, dims.B, H, dims.d):
-        raise ValueError(f"{name} must have shape {(dims.S, dims.B, H, dims.d)}, got {tuple(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != (S, B, H, d):
+        _refuse(t, name, torch.bfloat16, (S, B, H, d), dev)
     st = t.stride()
-    token = st[1] if dims.B > 1 else st[0] if dims.S > 1 else H * dims.d
-    if (dims.d > 1 and st[3] != 1) or (H > 1 and st[2] != dims.d) or (dims.S > 1 and st[0] != dims.B * token):
+    token = st[1] if B > 1 else st[0] if S > 1 else H * d
+    if st[3] != 1 or (H > 1 and st[2] != d) or (S > 1 and st[0] != B * token):
         raise ValueError(f"{name}: a token's heads must be contiguous and the tokens evenly spaced")
     return t.data_ptr(), token
 
@@ -461,28 +469,30 @@ def dsa_qk_norm_rope(q, k, v, q_out, k_out=None, v_out=None, stream=None, *, dim
     one pass (see include/dsa.h).  q, k, v: bf16 [S, B, H, d], possibly views into a packed
     projection; k and v go to k_out / v_out (contiguous) and / or the cache."""
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
-    bf = torch.bfloat16
-    r = dsa_rope(rope.rot, rope.interleaved, rope.eps, rope.scale, rope.inv_freq.data_ptr())
+    bf, dev = torch.bfloat16, torch.cuda.current_device()
     for w in (rope.q_norm, rope.k_norm):
         if w is not None and w.numel() != d:
             raise ValueError(f"norm weights must have {d} elements")
-    r.q_norm = None if rope.q_norm is None else rope.q_norm.data_ptr()
-    r.k_norm = None if rope.k_norm is None else rope.k_norm.data_ptr()
-    r.positions = _opt(positions, "positions", torch.int32, (S, B))
-    r.n_new = _opt(n_new, "n_new", torch.int32, (S,))
+    if rope.device != dev:
+        raise ValueError(f"rope is on cuda:{rope.device}, the current device is cuda:{dev}")
+    r = dsa_rope.from_buffer_copy(rope.c)
+    if positions is not None:
+        r.positions = _arg(positions, "positions", torch.int32, (S, B), dev)
+    if n_new is not None:
+        r.n_new = _arg(n_new, "n_new", torch.int32, (S,), dev)
     pq = pk = pv = None
     if q is not None:
-        pq, r.q_stride = _projection(q, "q", dims, Hq)
+        pq, r.q_stride = _projection(q, "q", S, B, Hq, d, dev)
     if k is not None:
-        pk, r.k_stride = _projection(k, "k", dims, Hkv)
+        pk, r.k_stride = _projection(k, "k", S, B, Hkv, d, dev)
     if v is not None:
-        pv, r.v_stride = _projection(v, "v", dims, Hkv)
+        pv, r.v_stride = _projection(v, "v", S, B, Hkv, d, dev)
     cache = (dims.n_phys, Hkv, dims.page, d)
     _call(load().dsa_qk_norm_rope(
-        pq, pk, pv, _opt(q_out, "q_out", bf, (S, B, Hq, d)), _opt(k_out, "k_out", bf, (S, B, Hkv, d)),
-        _opt(v_out, "v_out", bf, (S, B, Hkv, d)), _opt(k_cache, "k_cache", bf, cache),
-        _opt(v_cache, "v_cache", bf, cache), _raw_stream(stream), ctypes.byref(dims), ctypes.byref(r),
-        _opt(n_ctx, "n_ctx", torch.int32, (S,)), _ws(workspace), workspace.nbytes), "dsa_qk_norm_rope")
+        pq, pk, pv, _opt(q_out, "q_out", bf, (S, B, Hq, d), dev), _opt(k_out, "k_out", bf, (S, B, Hkv, d), dev),
+        _opt(v_out, "v_out", bf, (S, B, Hkv, d), dev), _opt(k_cache, "k_cache", bf, cache, dev),
+        _opt(v_cache, "v_cache", bf, cache, dev), _raw_stream(stream, dev), ctypes.byref(dims), ctypes.byref(r),
+        _opt(n_ctx, "n_ctx", torch.int32, (S,), dev), _ws(workspace, dev), workspace.nbytes), "dsa_qk_norm_rope")
 
 
 def window_workspace_size(dims: dsa_dims) -> int:
@@ -502,24 +512,24 @@ def dsa_window_attn(q_blk, k_cache, v_cache, blk_k, blk_v, o_out, stream=None, *
     """Attention with a sliding window and `sinks` first tokens that stay visible (see
     include/dsa.h).  blk_k = blk_v = None: the prefix alone."""
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
-    bf = torch.bfloat16
+    bf, dev = torch.bfloat16, torch.cuda.current_device()
     cache, blk = (dims.n_phys, Hkv, dims.page, d), (S, B, Hkv, d)
-    w = dsa_window(int(window), int(sinks), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,)))
-    dims = _with_lse_out(dims, lse_out)
+    w = dsa_window(int(window), int(sinks), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,), dev))
+    dims = _with_lse_out(dims, lse_out, dev)
     _call(load().dsa_window_attn(
-        _arg(q_blk, "q_blk", bf, (S, B, Hq, d)), _arg(k_cache, "k_cache", bf, cache),
-        _arg(v_cache, "v_cache", bf, cache), _opt(blk_k, "blk_k", bf, blk), _opt(blk_v, "blk_v", bf, blk),
-        _arg(o_out, "o_out", bf, (S, B, Hq, d)), _raw_stream(stream), ctypes.byref(dims), ctypes.byref(w),
-        _arg(n_ctx, "n_ctx", torch.int32, (S,)), _ws(workspace), workspace.nbytes), "dsa_window_attn")
+        _arg(q_blk, "q_blk", bf, (S, B, Hq, d), dev), _arg(k_cache, "k_cache", bf, cache, dev),
+        _arg(v_cache, "v_cache", bf, cache, dev), _opt(blk_k, "blk_k", bf, blk, dev), _opt(blk_v, "blk_v", bf, blk, dev),
+        _arg(o_out, "o_out", bf, (S, B, Hq, d), dev), _raw_stream(stream, dev), ctypes.byref(dims), ctypes.byref(w),
+        _arg(n_ctx, "n_ctx", torch.int32, (S,), dev), _ws(workspace, dev), workspace.nbytes), "dsa_window_attn")
 
 
-def _with_lse_out(dims: dsa_dims, lse_out) -> dsa_dims:
+def _with_lse_out(dims: dsa_dims, lse_out, dev) -> dsa_dims:
     """dims for one call with its log-sum-exp output: that of the argument, else none."""
     if lse_out is None and not dims.lse_out:
         return dims
     d = dsa_dims.from_buffer_copy(dims)
     if lse_out is not None:
-        d.lse_out = _arg(lse_out, "lse_out", torch.float32, (dims.S, dims.B, dims.Hq))
+        d.lse_out = _arg(lse_out, "lse_out", torch.float32, (dims.S, dims.B, dims.Hq), dev)
     return d
 
 
@@ -547,34 +557,33 @@ class Kv4Cache:
         scales = [torch.zeros((n_phys, Hkv, page, d // cls.GROUP), dtype=torch.bfloat16, device=dev) for _ in range(2)]
         return cls(*codes, *scales)
 
-    def _fits(self, dims):
+    def _fits(self, dims, dev):
         if self.shape != (dims.n_phys, dims.Hkv, dims.page, dims.d):
             raise ValueError(f"the 4-bit cache holds {self.shape}, dims say "
                              f"{(dims.n_phys, dims.Hkv, dims.page, dims.d)}")
-        if self.k.device.index != torch.cuda.current_device():
-            raise ValueError(f"the 4-bit cache is on {self.k.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+        if self.k.get_device() != dev:
+            raise ValueError(f"the 4-bit cache is on {self.k.device}, the current device is cuda:{dev}")
         return ctypes.byref(self.c)
 
 
 def dsa_kv4_store(blk_k, blk_v, cache: Kv4Cache, stream=None, *, dims: dsa_dims, n_ctx,
                   workspace: Workspace, n_new=None):
     """Appends the block's keys and values to the 4-bit cache at n_ctx[s] + b (see include/dsa.h)."""
-    bf, blk = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d)
+    bf, blk, dev = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d), torch.cuda.current_device()
     _call(load().dsa_kv4_store(
-        _arg(blk_k, "blk_k", bf, blk), _arg(blk_v, "blk_v", bf, blk), cache._fits(dims), _raw_stream(stream),
-        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (dims.S,)),
-        _opt(n_new, "n_new", torch.int32, (dims.S,)), _ws(workspace), workspace.nbytes), "dsa_kv4_store")
+        _arg(blk_k, "blk_k", bf, blk, dev), _arg(blk_v, "blk_v", bf, blk, dev), cache._fits(dims, dev), _raw_stream(stream, dev),
+        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (dims.S,), dev),
+        _opt(n_new, "n_new", torch.int32, (dims.S,), dev), _ws(workspace, dev), workspace.nbytes), "dsa_kv4_store")
 
 
 def dsa_kv4_load(cache: Kv4Cache, k_out, v_out, stream=None, *, dims: dsa_dims, start,
                  workspace: Workspace, n_new=None):
     """Reads tokens start[s] + b of the 4-bit cache back in bf16 (see include/dsa.h)."""
-    bf, blk = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d)
+    bf, blk, dev = torch.bfloat16, (dims.S, dims.B, dims.Hkv, dims.d), torch.cuda.current_device()
     _call(load().dsa_kv4_load(
-        cache._fits(dims), _arg(k_out, "k_out", bf, blk), _arg(v_out, "v_out", bf, blk), _raw_stream(stream),
-        ctypes.byref(dims), _arg(start, "start", torch.int32, (dims.S,)),
-        _opt(n_new, "n_new", torch.int32, (dims.S,)), _ws(workspace), workspace.nbytes), "dsa_kv4_load")
+        cache._fits(dims, dev), _arg(k_out, "k_out", bf, blk, dev), _arg(v_out, "v_out", bf, blk, dev), _raw_stream(stream, dev),
+        ctypes.byref(dims), _arg(start, "start", torch.int32, (dims.S,), dev),
+        _opt(n_new, "n_new", torch.int32, (dims.S,), dev), _ws(workspace, dev), workspace.nbytes), "dsa_kv4_load")
 
 
 def kv4_workspace_size(dims: dsa_dims) -> int:
@@ -593,15 +602,15 @@ def dsa_kv4_attn(q_blk, cache: Kv4Cache, idx, blk_k, blk_v, o_out, stream=None, 
     """The sparse pass over a 4-bit cache: the pages idx names, or every page where idx is None,
     and the block's own tokens (see include/dsa.h)."""
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
-    bf, blk = torch.bfloat16, (S, B, Hkv, d)
-    dims = _with_lse_out(dims, lse_out)
+    bf, blk, dev = torch.bfloat16, (S, B, Hkv, d), torch.cuda.current_device()
+    dims = _with_lse_out(dims, lse_out, dev)
     _call(load().dsa_kv4_attn(
-        _arg(q_blk, "q_blk", bf, (S, B, Hq, d)), cache._fits(dims),
-        _opt(idx, "idx", torch.int32, (S, Hkv, dims.kmax)), _opt(blk_k, "blk_k", bf, blk),
-        _opt(blk_v, "blk_v", bf, blk), _arg(o_out, "o_out", bf, (S, B, Hq, d)), _raw_stream(stream),
-        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (S,)),
-        _opt(idx_cnt, "idx_cnt", torch.int32, (S, Hkv)), _opt(n_new, "n_new", torch.int32, (S,)),
-        _ws(workspace), workspace.nbytes), "dsa_kv4_attn")
+        _arg(q_blk, "q_blk", bf, (S, B, Hq, d), dev), cache._fits(dims, dev),
+        _opt(idx, "idx", torch.int32, (S, Hkv, dims.kmax), dev), _opt(blk_k, "blk_k", bf, blk, dev),
+        _opt(blk_v, "blk_v", bf, blk, dev), _arg(o_out, "o_out", bf, (S, B, Hq, d), dev), _raw_stream(stream, dev),
+        ctypes.byref(dims), _arg(n_ctx, "n_ctx", torch.int32, (S,), dev),
+        _opt(idx_cnt, "idx_cnt", torch.int32, (S, Hkv), dev), _opt(n_new, "n_new", torch.int32, (S,), dev),
+        _ws(workspace, dev), workspace.nbytes), "dsa_kv4_attn")
 
 
 class DeviceWorkload:
