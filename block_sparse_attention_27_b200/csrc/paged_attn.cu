@@ -103,7 +103,7 @@ struct Params {
   int shared_out; // 1: equal shares of all tiles, 0: whole units
   int box_blk;    // block tokens of one TMA box
   Piece *piece;   // [CTA][2]: the unit that the CTA's share enters in its middle, the one it leaves
-  float *part_o;  // [CTA][2][rows][D]
+  float4 *part_o;  // [CTA][2][D/4][rows] x 4 columns
   float2 *part_ml;
 };
 
@@ -152,11 +152,24 @@ __device__ __forceinline__ uint32_t visible(int base, uint32_t len, int end, con
   if (base == kNever) return 0u;
   return below(base, end, len) & (below(base, w.sk, len) | (~below(base, w.lb, len) & below(base, w.hi + 1, len)));
 }
-// The same for 32 keys of a tile whose units of PAGE keys (or 128, a block tile) start at
-// the table's positions.
+// Bits j of word w below key k of the tile (0 <= k <= 128).
+__device__ __forceinline__ uint32_t first_bits(int k, int w) {
+  const int t = min(max(k - 32 * w, 0), 32);
+  uint32_t m;
+  asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(m) : "r"(t));  // (a shift by 32 leaves 0)
+  return ~m;
+}
+// Visible keys of a tile whose positions are base, base + 1, ...
+__device__ __forceinline__ void visible128(int base, int end, const Limits &w, uint32_t (&bits)[4]) {
+  auto at = [&](int x) { return x <= base ? 0 : (int)min((uint32_t)x - (uint32_t)base, (uint32_t)kBN); };
+  const int ke = at(end), ks = at(w.sk), kl = at(w.lb), kh = at(w.hi + 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bits[i] = first_bits(ke, i) & (first_bits(ks, i) | (~first_bits(kl, i) & first_bits(kh, i)));
+}
+// The same for 32 keys of a tile whose pages start at the table's positions.
 template <int PAGE>
-__device__ __forceinline__ uint32_t visible32(const int *pos, bool blk, int word, int end, const Limits &w) {
-  if (blk) return visible(pos[0] + 32 * word, 32, end, w);
+__device__ __forceinline__ uint32_t visible32(const int *pos, int word, int end, const Limits &w) {
   if (PAGE == 16)
     return visible(pos[2 * word], 16, end, w) | (visible(pos[2 * word + 1], 16, end, w) << 16);
   const int base = pos[32 * word / PAGE];
@@ -272,8 +285,10 @@ struct Stop {
       if (lane < PPT && lp != -1 && phys < 0) raise_status(prm.a.status, kStatusBadIndex);
       if (lane < PPT) tab[lane] = phys >= 0 ? lp * PAGE : kNever;
       const bool full = __all_sync(0xffffffffu, lane >= PPT || page_full(prm, lp, phys));
+      const int lp0 = __shfl_sync(0xffffffffu, lp, 0);
+      const bool row = __all_sync(0xffffffffu, lane >= PPT || (phys >= 0 && lp == lp0 + lane));
       if (lane == 0) {
-        tab[8] = full ? 1 : 0;
+        tab[8] = (full ? 1 : 0) | (row ? 4 : 0);  // 1: every row sees every key; 2: block tokens; 4: positions in a row
         tab[9] = ks.n;
       }
     }
@@ -377,7 +392,7 @@ __device__ __forceinline__ void cp_async_wait() {
 template <int D, int PAGE, bool KV4>
 __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     paged_attn(const __grid_constant__ Params prm, const __grid_constant__ CUtensorMap qmap,
-               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,  // boxes of a page, or of a tile's pages
                const __grid_constant__ CUtensorMap bkmap, const __grid_constant__ CUtensorMap bvmap) {
   using C = Cfg<D, KV4>;
   constexpr int ST = C::kStages;
@@ -626,12 +641,16 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             const int end = tab[9], st = k % ST;
             const Limits mine = row_limits<KV4>(a, ks.n, ks.b0 + r / sh.G);
             const Limits all{at.first.lb, at.last.hi, at.last.sk};  // keys that some row may see
+            if (flags & 6) {  // a block tile, or pages in a row
+              visible128(tab[0], end, mine, bits);
+            } else {
 #pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t b = visible32<PAGE>(tab, blk, w, end, mine);
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t b = visible32<PAGE>(tab, w, end, mine);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i == w) bits[i] = b;
+                for (int i = 0; i < 4; ++i)
+                  if (i == w) bits[i] = b;
+              }
             }
             // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
             alive = __all_sync(0xffffffffu, mbar_wait_short(v_full(st), (k / ST) & 1, ctx));
@@ -782,9 +801,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
               dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
                                   pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
           } else if (mine_row) {
-            float4 *dst = reinterpret_cast<float4 *>(prm.part_o + prow * D + c0);
+            const int rpt = prm.bpt * sh.G;
+            float4 *dst = prm.part_o + ((size_t)slot * (D / 4) + c0 / 4) * rpt + r;  // a warp's rows side by side
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) dst[i * rpt] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
           __syncwarp();  // the TMEM loads are warp-collective
         }
@@ -821,6 +841,9 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
           if (lane == 0) mbar_arrive(tab_full(k));
         }
         const uint32_t dst = ring + st * C::kTile;
+        const int p0 = __shfl_sync(0xffffffffu, phys, 0);
+        const bool run = !kBoxes && __all_sync(0xffffffffu, lane >= PPT || (phys >= 0 && phys == p0 + lane));
+        bool by_tma = t >= ks.pt;
         if (t >= ks.pt) {
           int u_end;
           bool f;
@@ -829,6 +852,14 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             mbar_arrive_expect_tx(full(st), (uint32_t)prm.box_blk * 128u * C::kHalves);
             for (int hf = 0; hf < C::kHalves; ++hf)
               tma_load_3d(dst + hf * C::kHalf, bmap, full(st), hf * 64, ks.h, ks.s * sh.B + u0);
+          } else {
+            mbar_arrive(full(st));
+          }
+        } else if (run) {  // the tile's pages lie one after the other: one box per half
+          by_tma = true;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full(st), C::kTile);
+            for (int hf = 0; hf < C::kHalves; ++hf) tma_load_4d(dst + hf * C::kHalf, map, full(st), hf * 64, 0, ks.h, p0);
           } else {
             mbar_arrive(full(st));
           }
@@ -869,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
               mbar_arrive(full((k - 1) % ST));
             }
           }
-          told = t >= ks.pt ? k + 1 : k;  // tiles whose arrivals are made
+          told = by_tma ? k + 1 : k;  // tiles whose arrivals are made
         }
         lp = lp1;
         phys = phys1;
@@ -1507,7 +1538,8 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, FewCfg<D, KV4, N
     const int slot = 2 * blockIdx.x + (at.begins() ? 1 : 0);
     if (!whole && threadIdx.x == 0) prm.piece[slot] = Piece{at.unit, at.begins(), at.ends(), 0};
     for (int e = threadIdx.x; e < ks.rows * (D / 4); e += M::kThreads) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      // whole rows one after the other; a piece's side by side
+      const int r = whole ? e / (D / 4) : e % ks.rows, c = (whole ? e % (D / 4) : e / ks.rows) * 4;
       float mx = -INFINITY, L = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -1531,7 +1563,7 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, FewCfg<D, KV4, N
         *reinterpret_cast<uint2 *>(a.o_out + orow * D + c) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
         if (c == 0 && sh.lse_out) sh.lse_out[orow] = L != 0.f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;
       } else {
-        *reinterpret_cast<float4 *>(prm.part_o + prow * D + c) = y;
+        prm.part_o[((size_t)slot * (D / 4) + c / 4) * (prm.bpt * sh.G) + r] = y;
         if (c == 0) prm.part_ml[prow] = make_float2(mx, L);
       }
     }
@@ -1539,9 +1571,9 @@ __global__ void __launch_bounds__(FewCfg<D, KV4, NT>::kThreads, FewCfg<D, KV4, N
   }
 }
 
-// Joins the pieces of the units that shares cut: block x = c - 1 takes the unit that CTA
-// c - 1 began and left (its later pieces are the first ones of CTAs c, c + 1, ...); a warp
-// per row, D/32 columns a lane.  The pieces are joined in their order.
+// Joins the pieces of the units that shares cut: block x takes the unit that CTA x began and
+// left (its later pieces are the first ones of CTAs x + 1, x + 2, ...); a thread has four
+// columns of a row.  The pieces are joined in their order.
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_constant__ Params prm) {
@@ -1550,15 +1582,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_consta
   const Shape &sh = prm.sh;
   const int rpt = prm.bpt * sh.G;  // rows of a unit
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
   const Piece p = prm.piece[2 * blockIdx.x + 1];
-  if (p.unit < 0 || r >= rpt) return;
-  const int rt = p.unit % prm.rowtiles, h = p.unit / prm.rowtiles % sh.Hkv, s = p.unit / prm.rowtiles / sh.Hkv;
-  const int b = rt * prm.bpt + r / sh.G;
-  if (b >= block_tokens(prm.a.n_new, s, sh.B, prm.a.status, false)) return;
-  constexpr int E = D / 32;
-  // the pieces: slot 2 c + 1 of CTA c = x, then slots 2 (c + 1), ... to the one that ends the
-  // unit; a lane looks at one each, so that the chain costs one round of loads per 32
+  if (p.unit < 0) return;
+  // the pieces: slot 2 x + 1, then slots 2 (x + 1), ... to the one that ends the unit; a lane
+  // looks at one each, so that the chain costs one round of loads per 32
   int count = 0;
   for (int i0 = 0;; i0 += 32) {
     const int c = blockIdx.x + i0 + lane;
@@ -1568,20 +1595,22 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_consta
     if (found) break;
   }
   count = min(count, (int)gridDim.x + 1 - (int)blockIdx.x);  // (a call that gave up may have left no end)
-  float M = -INFINITY, L = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto row_of = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * rpt + r; };
+  const int rt = p.unit % prm.rowtiles, h = p.unit / prm.rowtiles % sh.Hkv, s = p.unit / prm.rowtiles / sh.Hkv;
+  const int e = blockIdx.y * kMergeThreads + threadIdx.x, c4 = e / rpt, r = e % rpt;
+  const int b = rt * prm.bpt + r / sh.G;
+  if (c4 >= D / 4 || b >= block_tokens(prm.a.n_new, s, sh.B, prm.a.status, false)) return;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < count; i0 += 8) {
     float2 ml[8];
-    float v[8][E];
+    float4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       ml[i] = make_float2(-INFINITY, 0.f);
       if (i0 + i >= count) continue;
-      ml[i] = prm.part_ml[row_of(i0 + i)];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = prm.part_o[row_of(i0 + i) * D + lane * E + e];
+      const size_t slot = i0 + i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i0 + i);
+      ml[i] = prm.part_ml[slot * rpt + r];
+      v[i] = prm.part_o[(slot * (D / 4) + c4) * rpt + r];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -1590,16 +1619,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const __grid_consta
       const float sc = M == -INFINITY ? 0.f : exp2f(M - mn), wt = ml[i].x == -INFINITY ? 1.f : exp2f(ml[i].x - mn);
       M = mn;
       L = fmaf(L, sc, wt * ml[i].y);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], sc, wt * v[i][e]);
+      o.x = fmaf(o.x, sc, wt * v[i].x); o.y = fmaf(o.y, sc, wt * v[i].y);
+      o.z = fmaf(o.z, sc, wt * v[i].z); o.w = fmaf(o.w, sc, wt * v[i].w);
     }
   }
   const size_t orow = ((size_t)s * sh.B + b) * sh.Hq + (size_t)h * sh.G + r % sh.G;
   const float inv = L != 0.f ? 1.f / L : 0.f;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(prm.a.o_out + orow * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  if (sh.lse_out && lane == 0) sh.lse_out[orow] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  *reinterpret_cast<uint2 *>(prm.a.o_out + orow * D + 4 * c4) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (sh.lse_out && c4 == 0) sh.lse_out[orow] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 struct Geometry {
@@ -1656,13 +1683,12 @@ cudaError_t launch_typed(const Shape &sh, const PagedPlan &plan, const PagedArgs
   unsigned char *ws = reinterpret_cast<unsigned char *>(a.status) + kWorkspaceHeader;
   const size_t slots = 2 * (size_t)plan.ctas;
   prm.piece = reinterpret_cast<Piece *>(ws);
-  prm.part_o = reinterpret_cast<float *>(ws + slots * sizeof(Piece));
-  prm.part_ml = reinterpret_cast<float2 *>(prm.part_o + slots * g.rows * D);
+  prm.part_o = reinterpret_cast<float4 *>(ws + slots * sizeof(Piece));
+  prm.part_ml = reinterpret_cast<float2 *>(prm.part_o + slots * g.rows * (D / 4));
   auto join = [&](cudaError_t e) {
     if (e != cudaSuccess || plan.launches == 1) return e;
-    constexpr int kWarps = kMergeThreads / 32;
-    return launch_pdl(paged_merge<D>, dim3((unsigned)(plan.ctas - 1), (unsigned)((g.rows + kWarps - 1) / kWarps)), kMergeThreads,
-                      0, stream, prm);
+    return launch_pdl(paged_merge<D>, dim3((unsigned)(plan.ctas - 1), (unsigned)((g.rows * (D / 4) + kMergeThreads - 1) / kMergeThreads)),
+                      kMergeThreads, 0, stream, prm);
   };
   if (plan.few)
     return join(g.rows <= 8 ? launch_few<D, PAGE, KV4, 1>(prm, plan, stream) : launch_few<D, PAGE, KV4, 2>(prm, plan, stream));
@@ -1672,7 +1698,10 @@ cudaError_t launch_typed(const Shape &sh, const PagedPlan &plan, const PagedArgs
   CUtensorMap q{}, k{}, v{}, bk{}, bv{};
   const long long tokens = (long long)sh.S * sh.B;
   if ((err = make_q_tensor_map(&q, a.q, tokens, sh.Hq, D, sh.G, g.bpt)) != cudaSuccess) return err;
-  if (!KV4 && PAGE >= 64) {
+  if (!KV4 && PAGE < 64) {
+    if ((err = make_kv_pages_tensor_map(&k, a.k, sh.n_phys, sh.Hkv, PAGE, D, kBN / PAGE)) != cudaSuccess) return err;
+    if ((err = make_kv_pages_tensor_map(&v, a.v, sh.n_phys, sh.Hkv, PAGE, D, kBN / PAGE)) != cudaSuccess) return err;
+  } else if (!KV4) {
     const long long nrows = sh.n_phys * sh.Hkv * PAGE;
     if ((err = make_kv_tensor_map(&k, a.k, nrows, D, PAGE)) != cudaSuccess) return err;
     if ((err = make_kv_tensor_map(&v, a.v, nrows, D, PAGE)) != cudaSuccess) return err;
