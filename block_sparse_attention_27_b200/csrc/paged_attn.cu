@@ -763,7 +763,10 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         alive = __all_sync(0xffffffffu, mbar_wait_short(o_full, it & 1, ctx));
         if (!alive) break;
         tc_fence_after();
-        if (!meet_all()) break;  // m_ref is final
+        // m_ref is final once the last tile is decided (its barrier's next phase is a tile of
+        // the next stop, which this thread has not begun)
+        alive = __all_sync(0xffffffffu, mbar_wait_short(decided(k1 - 1), ((k1 - 1) >> 1) & 1, ctx));
+        if (!alive) break;
         const float M = m_ref[r];
         if (m_used != M) l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
         if (g == 1) l_x[r] = l;
