@@ -195,6 +195,11 @@ CASES = {
     "padded": dict(S=3, B=20, Hq=4, Hkv=1, d=128, page=16, n=[40, 0, 300], new=[20, 0, 3]),
     "padded_decode": dict(S=3, B=1, Hq=4, Hkv=1, d=128, page=16, n=[40, 10, 300], new=[1, 0, 1]),
     "identity": dict(S=3, B=2, Hq=4, Hkv=2, d=128, page=32, n=[64, 200, 31], table=False),
+    "rows_12": dict(S=2, B=3, Hq=8, Hkv=2, d=128, page=32, n=[500, 129]),
+    "rows_16_sparse": dict(S=2, B=4, Hq=8, Hkv=2, d=128, page=16, n=[500, 129], kp=7),
+    "few_rows_padded": dict(S=4, B=2, Hq=4, Hkv=2, d=64, page=16, n=[500, 0, 1, 257], new=[2, 2, 0, 1]),
+    "many_units": dict(S=200, B=1, Hq=8, Hkv=8, d=64, page=16, n=[(7 * i) % 100 for i in range(200)]),
+    "long_block": dict(S=1, B=20, Hq=1, Hkv=1, d=64, page=16, n=[6001]),
     "long": dict(S=1, B=2, Hq=2, Hkv=1, d=128, page=16, n=[6001]),
 }
 

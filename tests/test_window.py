@@ -96,6 +96,19 @@ CASES = {
     "prefix_alone": dict(S=3, B=8, Hq=4, Hkv=2, d=128, page=16, n=[0, 3, 200], window=5, sinks=0, causal=False, block=False),
     "prefix_alone_long": dict(S=1, B=32, Hq=8, Hkv=2, d=128, page=16, n=[2000], window=1100, sinks=33, causal=True, block=False),
     "identity_table": dict(S=3, B=4, Hq=4, Hkv=2, d=128, page=32, n=[700, 64, 65], window=300, sinks=8, causal=True, table=False),
+    # at most 16 rows per KV head and tables of every kind, the other kernel's page sizes
+    "few_rows_9_to_16": dict(S=2, B=3, Hq=8, Hkv=2, d=128, page=16, n=[400, 90], window=130, sinks=5, causal=True),
+    "few_rows_both_ways": dict(S=2, B=16, Hq=2, Hkv=2, d=64, page=32, n=[200, 33], window=9, sinks=2, causal=False),
+    "few_rows_p64": dict(S=3, B=1, Hq=7, Hkv=1, d=64, page=64, n=[1000, 63, 64], window=300, sinks=100, causal=True),
+    "few_rows_long": dict(S=1, B=2, Hq=2, Hkv=1, d=128, page=16, n=[6001], window=1 << 20, sinks=0, causal=True),
+    "rows_17": dict(S=1, B=17, Hq=1, Hkv=1, d=128, page=64, n=[300], window=200, sinks=7, causal=True),
+    "identity_table_wide": dict(S=2, B=20, Hq=4, Hkv=2, d=128, page=16, n=[700, 129], window=400, sinks=20, causal=False, table=False),
+    "identity_table_wide_p32": dict(S=2, B=20, Hq=4, Hkv=2, d=64, page=32, n=[700, 129], window=400, sinks=20, causal=True, table=False),
+    "identity_table_wide_p64": dict(S=1, B=20, Hq=4, Hkv=2, d=128, page=64, n=[513], window=1000, sinks=0, causal=True, table=False),
+    "many_units_few_rows": dict(S=200, B=1, Hq=8, Hkv=8, d=64, page=16, n=[i % 150 for i in range(200)], window=100, sinks=3,
+                                causal=True),
+    "many_units": dict(S=75, B=20, Hq=16, Hkv=16, d=64, page=16, n=[i % 9 for i in range(75)], window=6, sinks=3, causal=True,
+                       new=[20 - i % 21 for i in range(75)]),
     "large_scores": dict(S=1, B=16, Hq=4, Hkv=1, d=128, page=16, n=[600], window=500, sinks=8, causal=True, scale=4.0),
 }
 
