@@ -929,7 +929,6 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     const int tid = (threadIdx.x - 320) & 63;
     constexpr int GR = D / kKv4Group;            // groups of a row
     constexpr int CH = kBN * GR / 64;            // 16-byte chunks of a thread
-    constexpr int RPS = 16 / (2 * GR);           // rows whose scales are 16 bytes
     const uint8_t *codes = isv ? a.kv4.v : a.kv4.k;
     const __nv_bfloat16 *scales = isv ? a.kv4.vs : a.kv4.ks;
     const CUtensorMap *bmap = isv ? &bvmap : &bkmap;
@@ -956,19 +955,19 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         lp[i] = ph[i] = -1;
         if (i < nt && lane < PPT) at.page_at(prm, t0 + i, lane, lp[i], ph[i]);
       }
+      // PAGE / 2 threads bring a page: its codes are consecutive, 16 bytes a thread and step
       auto load = [&](int slot, int phys) {
-        const uint32_t dst = base + rawring + slot * C::kRaw;
-#pragma unroll 2
-        for (int i = 0; i < CH; ++i) {
-          const int c = tid + 64 * i, key = c / GR;
-          const int p = __shfl_sync(0xffffffffu, phys, key / PAGE);
-          if (p >= 0)
-            cp_async16(dst + c * 16, codes + (((long long)p * sh.Hkv + ks.h) * PAGE + key % PAGE) * (D / 2) + (c % GR) * 16);
+        const int e = tid / (PAGE / 2), at0 = tid % (PAGE / 2);
+        const int p = __shfl_sync(0xffffffffu, phys, e);
+        if (p >= 0) {
+          const uint32_t dst = base + rawring + slot * C::kRaw + e * (PAGE * D / 2) + at0 * 16;
+          const uint8_t *src = codes + ((long long)p * sh.Hkv + ks.h) * (PAGE * D / 2) + at0 * 16;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) cp_async16(dst + i * (PAGE / 2) * 16, src + i * (PAGE / 2) * 16);
+          if (at0 < PAGE * GR / 8)
+            cp_async16(base + rawring + slot * C::kRaw + C::kRawCodes + e * (PAGE * GR * 2) + at0 * 16,
+                       scales + ((long long)p * sh.Hkv + ks.h) * (PAGE * GR) + at0 * 8);
         }
-        const int key = tid * RPS;
-        const int p = __shfl_sync(0xffffffffu, phys, min(key, kBN - 1) / PAGE);
-        if (key < kBN && p >= 0)
-          cp_async16(dst + C::kRawCodes + tid * 16, scales + (((long long)p * sh.Hkv + ks.h) * PAGE + key % PAGE) * GR);
         cp_async_commit();
       };
       if (!gather()) break;  // all of the 64 threads have read the piece before
@@ -1001,27 +1000,38 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             mbar_arrive(full(st));
           }
         } else {
+          // chunk i of a thread: group grp of key key0 + i 64/GR; the swizzle of its row is
+          // the same for every i
+          const int key0 = tid / GR, grp = tid % GR;
           const unsigned char *src = smem + rawring + (k % 3) * C::kRaw;
-          unsigned char *dst = smem + ring + st * C::kTile;
-#pragma unroll 2
-          for (int i = 0; i < CH; ++i) {
-            const int c = tid + 64 * i, key = c / GR, grp = c % GR;
-            const int p = __shfl_sync(0xffffffffu, ph[0], key / PAGE), q = __shfl_sync(0xffffffffu, lp[0], key / PAGE);
-            const bool on = p >= 0 && q * PAGE + key % PAGE < ks.n;
-            uint4 w = *reinterpret_cast<const uint4 *>(src + c * 16);
-            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + c * 2);
+          unsigned char *dst = smem + ring + st * C::kTile + (grp / 2) * C::kHalf;
+          const bool whole = __all_sync(0xffffffffu, lane >= PPT || (ph[0] >= 0 && (lp[0] + 1) * PAGE <= ks.n));
+          auto unpack = [&](int i, bool on) {
+            uint4 w = *reinterpret_cast<const uint4 *>(src + (tid + 64 * i) * 16);
+            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + (tid + 64 * i) * 2);
             __nv_bfloat162 s8, m24;
-            kv4_constants(sc, s8, m24);
+            kv4_constants(__bfloat162bfloat162(sc), s8, m24);
             if (!on) {  // code 8 with scale 0 is the value 0
               w = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
               s8 = m24 = __float2bfloat162_rn(0.f);
             }
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
-              *reinterpret_cast<uint4 *>(dst + (grp / 2) * C::kHalf + sw128_offset(key, (grp % 2) * 4 + q4)) =
-                  make_uint4(kv4_pair(ww[q4], 0, s8, m24), kv4_pair(ww[q4], 1, s8, m24), kv4_pair(ww[q4], 2, s8, m24),
-                             kv4_pair(ww[q4], 3, s8, m24));
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4 *>(dst + i * (64 / GR) * 128 + sw128_offset(key0, (grp % 2) * 4 + q)) =
+                  make_uint4(kv4_pair(ww[q], 0, s8, m24), kv4_pair(ww[q], 1, s8, m24), kv4_pair(ww[q], 2, s8, m24),
+                             kv4_pair(ww[q], 3, s8, m24));
+          };
+          if (whole) {
+#pragma unroll 4
+            for (int i = 0; i < CH; ++i) unpack(i, true);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < CH; ++i) {
+              const int key = key0 + i * (64 / GR);
+              const int p = __shfl_sync(0xffffffffu, ph[0], key / PAGE), q = __shfl_sync(0xffffffffu, lp[0], key / PAGE);
+              unpack(i, p >= 0 && q * PAGE + key % PAGE < ks.n);
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(full(st));
