@@ -1002,13 +1002,16 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         } else {
           // chunk i of a thread: group grp of key key0 + i 64/GR; the swizzle of its row is
           // the same for every i
-          const int key0 = tid / GR, grp = tid % GR;
+          // (d = 128: eight lanes are four keys x two groups of one half, so that their stores
+          // meet eight different banks of 16 bytes)
+          const int key0 = GR == 4 ? (tid >> 5) * 8 + ((tid >> 4) & 1) * 4 + ((tid >> 1) & 3) : tid / GR;
+          const int grp = GR == 4 ? ((tid >> 3) & 1) * 2 + (tid & 1) : tid % GR, at0 = key0 * GR + grp;
           const unsigned char *src = smem + rawring + (k % 3) * C::kRaw;
           unsigned char *dst = smem + ring + st * C::kTile + (grp / 2) * C::kHalf;
           const bool whole = __all_sync(0xffffffffu, lane >= PPT || (ph[0] >= 0 && (lp[0] + 1) * PAGE <= ks.n));
           auto unpack = [&](int i, bool on) {
-            uint4 w = *reinterpret_cast<const uint4 *>(src + (tid + 64 * i) * 16);
-            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + (tid + 64 * i) * 2);
+            uint4 w = *reinterpret_cast<const uint4 *>(src + (at0 + 64 * i) * 16);
+            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + (at0 + 64 * i) * 2);
             __nv_bfloat162 s8, m24;
             kv4_constants(__bfloat162bfloat162(sc), s8, m24);
             if (!on) {  // code 8 with scale 0 is the value 0
