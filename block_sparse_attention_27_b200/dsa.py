@@ -346,6 +346,9 @@ def dsa_merge_attn(o_a, lse_a, o_b, lse_b, o_out, lse_out=None, stream=None):
 
 
 # ------------------------------------------- operators beside the two passes ----
+_INT32_MAX = 2 ** 31 - 1  # a window or a count of sinks past it is past every position
+
+
 # A call's host time counts where its kernel takes a few microseconds: each tensor is checked
 # in one expression, and the reason is worked out only where that fails.
 def _refuse(t, name, dtype, shape, dev):
@@ -363,6 +366,8 @@ def _refuse(t, name, dtype, shape, dev):
 def _arg(t, name, dtype, shape=None, dev=None):
     """Address of a contiguous tensor of that type and shape on the current device."""
     if dev is None:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
         dev = torch.cuda.current_device()
     if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev
             or (shape is not None and t.shape != shape) or not t.is_contiguous()):
@@ -403,6 +408,8 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, device="cuda"):
     """
     if rot < 8 or rot % 8:
         raise ValueError("rot must be a positive multiple of 8")
+    if not base > 1:
+        raise ValueError("the base must be greater than 1")
     i = torch.arange(rot // 2, dtype=torch.float64)
     freq, scale = float(base) ** (-2 * i / rot), 1.0
     if scaling is not None:
@@ -500,7 +507,8 @@ def window_workspace_size(dims: dsa_dims) -> int:
 
 
 def window_launches(dims: dsa_dims, window, sinks=0, causal=False) -> int:
-    rc = int(load().dsa_window_launches(ctypes.byref(dims), ctypes.byref(dsa_window(window, sinks, int(causal), None))))
+    rc = int(load().dsa_window_launches(ctypes.byref(dims), ctypes.byref(dsa_window(
+        min(int(window), _INT32_MAX), min(int(sinks), _INT32_MAX), int(bool(causal)), None))))
     if rc < 0:
         raise DsaError(rc, "dsa_window_launches")
     return rc
@@ -514,7 +522,7 @@ def dsa_window_attn(q_blk, k_cache, v_cache, blk_k, blk_v, o_out, stream=None, *
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
     bf, dev = torch.bfloat16, torch.cuda.current_device()
     cache, blk = (dims.n_phys, Hkv, dims.page, d), (S, B, Hkv, d)
-    w = dsa_window(int(window), int(sinks), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,), dev))
+    w = dsa_window(min(int(window), _INT32_MAX), min(int(sinks), _INT32_MAX), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,), dev))
     dims = _with_lse_out(dims, lse_out, dev)
     _call(load().dsa_window_attn(
         _arg(q_blk, "q_blk", bf, (S, B, Hq, d), dev), _arg(k_cache, "k_cache", bf, cache, dev),

@@ -250,6 +250,7 @@ def test_refusals_on_host(lib):
     assert need >= dsa.WORKSPACE_HEADER_BYTES and rc(nbytes=dsa.WORKSPACE_HEADER_BYTES - 1) == dsa.DSA_ERR_WORKSPACE_TOO_SMALL
     assert dsa.window_workspace_size(dsa.make_dims(**{**base, "d": 96})) == 0
     assert dsa.window_launches(dsa.make_dims(**base), 64) >= 1
+    assert dsa.window_launches(dsa.make_dims(**base), 1 << 40, 1 << 35) >= 1  # past every position, not wrapped
     with pytest.raises(dsa.DsaError):
         dsa.window_launches(dsa.make_dims(**base), 0)
 
