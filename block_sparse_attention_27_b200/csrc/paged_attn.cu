@@ -20,7 +20,7 @@
 //   1        TMEM; the MMAs
 //   2..9     two softmax groups of 128 threads, a thread per row, alternate tiles
 //   10, 11   V tiles; the queries
-//   4-bit cache: 0 the queries, 10..11 and 12..13 unpack K and V rows into bf16 tiles
+//   4-bit cache: 0 the queries, 10..12 and 13..15 unpack K and V rows into bf16 tiles
 //
 //   S = Q K^T (128 x 128) into one of three TMEM buffers, P = 2^(S - m) in bf16 over its
 //   first 64 columns, O += P V (TMEM).  S runs two tiles ahead of P.
@@ -64,7 +64,7 @@ template <int D, bool KV4>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kStages = KV4 ? 2 : D == 128 ? 3 : 5;
-  static constexpr int kThreads = KV4 ? 448 : 384;
+  static constexpr int kThreads = KV4 ? 512 : 384;
   static constexpr uint32_t kHalf = 128u * 128u;           // 128 rows x 128 B
   static constexpr uint32_t kTile = kHalves * kHalf;       // one K or V tile, or Q
   static constexpr uint32_t kOffQ = 0;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   constexpr int ST = C::kStages;
   constexpr int PPT = kBN / PAGE;      // pages of a tile
   constexpr bool kBoxes = PAGE >= 64;  // bf16 pages come by TMA
-  constexpr uint32_t kLoaders = KV4 ? 64 : 32;  // threads that fill K, and that fill V
+  constexpr uint32_t kLoaders = KV4 ? 96 : 32;  // threads that fill K, and that fill V
   extern __shared__ unsigned char smem_raw[];
   const Shape &sh = prm.sh;
   const PagedArgs &a = prm.a;
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     mbar_init(o_full, 1);
     mbar_init(o_free, 64 * aw);
     mbar_init(meet, 64 * aw);
-    mbar_init(loaders(false), 64);
-    mbar_init(loaders(true), 64);
+    mbar_init(loaders(false), kLoaders);
+    mbar_init(loaders(true), kLoaders);
     mbar_init(drain, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(stop_full(i), 1);
@@ -922,13 +922,14 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------- 4-bit rows into bf16 tiles --
-    // 64 threads each for K and V.  Packed tiles come in by 16-byte asynchronous copies,
-    // two tiles ahead; a thread then turns 16 bytes (a group of 32 values) at a time into
-    // 64 bytes of a swizzled row.
-    const bool isv = warp >= 12;
-    const int tid = (threadIdx.x - 320) & 63;
+    // Three warps each for K and V.  Packed tiles come in by 16-byte asynchronous copies, two
+    // tiles ahead; a lane then turns 16 bytes (a group of 32 values) at a time into 64 bytes
+    // of a swizzled row.  A warp alone on its scheduler waits for most of its instructions:
+    // unpacking took 2.7 of 4.1 thousand cycles a tile in two warps.
+    const bool isv = warp >= 13;
+    const int tid = threadIdx.x - (isv ? 416 : 320);
     constexpr int GR = D / kKv4Group;            // groups of a row
-    constexpr int CH = kBN * GR / 64;            // 16-byte chunks of a thread
+    constexpr int CH = kBN * GR / 64;            // 16-byte copies of each of 64 threads
     const uint8_t *codes = isv ? a.kv4.v : a.kv4.k;
     const __nv_bfloat16 *scales = isv ? a.kv4.vs : a.kv4.ks;
     const CUtensorMap *bmap = isv ? &bvmap : &bkmap;
@@ -938,7 +939,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     const uint32_t rawring = C::kOffRaw + (isv ? C::kRawSlots * C::kRaw : 0);
     int k = 0, gathered = 0;
     bool ok = true;
-    auto gather = [&]() {  // the 64 threads; a bounded wait, unlike a named barrier
+    auto gather = [&]() {  // the three warps; a bounded wait, unlike a named barrier
       mbar_arrive(loaders(isv));
       ok = __all_sync(0xffffffffu, mbar_wait_short(loaders(isv), gathered & 1, ctx));
       ++gathered;
@@ -955,11 +956,11 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         lp[i] = ph[i] = -1;
         if (i < nt && lane < PPT) at.page_at(prm, t0 + i, lane, lp[i], ph[i]);
       }
-      // PAGE / 2 threads bring a page: its codes are consecutive, 16 bytes a thread and step
+      // PAGE / 2 of 64 threads bring a page: its codes are consecutive, 16 bytes a thread and step
       auto load = [&](int slot, int phys) {
         const int e = tid / (PAGE / 2), at0 = tid % (PAGE / 2);
-        const int p = __shfl_sync(0xffffffffu, phys, e);
-        if (p >= 0) {
+        const int p = __shfl_sync(0xffffffffu, phys, e & 31);
+        if (tid < 64 && p >= 0) {
           const uint32_t dst = base + rawring + slot * C::kRaw + e * (PAGE * D / 2) + at0 * 16;
           const uint8_t *src = codes + ((long long)p * sh.Hkv + ks.h) * (PAGE * D / 2) + at0 * 16;
 #pragma unroll
@@ -970,7 +971,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         }
         cp_async_commit();
       };
-      if (!gather()) break;  // all of the 64 threads have read the piece before
+      if (!gather()) break;  // all three warps have read the piece before
       load(k % 3, ph[0]);
       load((k + 1) % 3, ph[1]);
       for (int j = 0; j < nt; ++j, ++k) {
@@ -983,7 +984,7 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         load((k + 2) % 3, ph[2]);
         if (k >= ST) ok = __all_sync(0xffffffffu, mbar_wait_short(empty(st), ((k / ST) - 1) & 1, ctx));
         if (!ok) break;
-        if (warp == 10) {
+        if (warp == 12) {  // of K's warps the one with a pass less to unpack
           at.put_table(prm, table(k), t, lane, lp[0], ph[0]);
           __syncwarp();
           if (lane == 0) mbar_arrive(tab_full(k));
@@ -1000,18 +1001,18 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             mbar_arrive(full(st));
           }
         } else {
-          // chunk i of a thread: group grp of key key0 + i 64/GR; the swizzle of its row is
-          // the same for every i
-          // (d = 128: eight lanes are four keys x two groups of one half, so that their stores
-          // meet eight different banks of 16 bytes)
-          const int key0 = GR == 4 ? (tid >> 5) * 8 + ((tid >> 4) & 1) * 4 + ((tid >> 1) & 3) : tid / GR;
-          const int grp = GR == 4 ? ((tid >> 3) & 1) * 2 + (tid & 1) : tid % GR, at0 = key0 * GR + grp;
+          // A warp's pass is 32 groups of 32 / GR keys, one a lane; the swizzle of a lane's row
+          // is the same in every pass.  (d = 128: eight lanes are four keys x two groups of one
+          // half, so that their stores meet eight different banks of 16 bytes.)
+          constexpr int kKeys = 32 / GR, kPasses = kBN / kKeys;
+          const int key0 = GR == 4 ? ((lane >> 4) & 1) * 4 + ((lane >> 1) & 3) : lane / GR;
+          const int grp = GR == 4 ? ((lane >> 3) & 1) * 2 + (lane & 1) : lane % GR, at0 = key0 * GR + grp;
           const unsigned char *src = smem + rawring + (k % 3) * C::kRaw;
           unsigned char *dst = smem + ring + st * C::kTile + (grp / 2) * C::kHalf;
           const bool whole = __all_sync(0xffffffffu, lane >= PPT || (ph[0] >= 0 && (lp[0] + 1) * PAGE <= ks.n));
           auto unpack = [&](int i, bool on) {
-            uint4 w = *reinterpret_cast<const uint4 *>(src + (at0 + 64 * i) * 16);
-            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + (at0 + 64 * i) * 2);
+            uint4 w = *reinterpret_cast<const uint4 *>(src + (at0 + 32 * i) * 16);
+            const __nv_bfloat16 sc = *reinterpret_cast<const __nv_bfloat16 *>(src + C::kRawCodes + (at0 + 32 * i) * 2);
             __nv_bfloat162 s8, m24;
             kv4_constants(__bfloat162bfloat162(sc), s8, m24);
             if (!on) {  // code 8 with scale 0 is the value 0
@@ -1021,17 +1022,17 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(dst + i * (64 / GR) * 128 + sw128_offset(key0, (grp % 2) * 4 + q)) =
+              *reinterpret_cast<uint4 *>(dst + i * kKeys * 128 + sw128_offset(key0, (grp % 2) * 4 + q)) =
                   make_uint4(kv4_pair(ww[q], 0, s8, m24), kv4_pair(ww[q], 1, s8, m24), kv4_pair(ww[q], 2, s8, m24),
                              kv4_pair(ww[q], 3, s8, m24));
           };
           if (whole) {
-#pragma unroll 4
-            for (int i = 0; i < CH; ++i) unpack(i, true);
+#pragma unroll 2
+            for (int i = tid >> 5; i < kPasses; i += 3) unpack(i, true);
           } else {
 #pragma unroll 1
-            for (int i = 0; i < CH; ++i) {
-              const int key = key0 + i * (64 / GR);
+            for (int i = tid >> 5; i < kPasses; i += 3) {
+              const int key = key0 + i * kKeys;
               const int p = __shfl_sync(0xffffffffu, ph[0], key / PAGE), q = __shfl_sync(0xffffffffu, lp[0], key / PAGE);
               unpack(i, p >= 0 && q * PAGE + key % PAGE < ks.n);
             }
