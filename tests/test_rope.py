@@ -78,6 +78,57 @@ def test_against_definition(lib, S, B, Hq, Hkv, d, rot, inter, norm, start):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,rot,inter,norm", [
+    (3, 1, 128, 64, False, True),
+    (6, 2, 64, 64, True, True),
+    (2, 1, 128, 24, False, False),
+    (6, 3, 64, 16, False, True),
+    (1, 1, 64, 56, True, True),
+    (8, 2, 128, 128, True, False),
+])
+def test_many_tokens(lib, Hq, Hkv, d, rot, inter, norm):
+    """A long padded batch, which takes several tokens a block of threads: the definition, and the
+    rows past n_new left as they were; the cache gets what the outputs get."""
+    S, B, page = 2, 1303, 32
+    qkv, w = inputs(S, B, Hq, Hkv, d, 3)
+    n = torch.tensor([7, 70000], dtype=torch.int32)
+    new = [1303, 1290]
+    max_pages = 2300
+    table = (torch.arange(2 * 42, dtype=torch.int32).view(2, 42)).flip(1)
+    tab = torch.full((2, max_pages), -1, dtype=torch.int32)
+    tab[0, :42], tab[1, 70000 // page:70000 // page + 42] = table[0], table[1]
+    inv, _ = dsa.rope_inv_freq(rot, 1e5)
+    dev = qkv.cuda()
+    q, k, v = views(dev, S, B, Hq, Hkv, d)
+    qo, ko, vo = (torch.full((S, B, H, d), 7.0, dtype=BF, device="cuda") for H in (Hq, Hkv, Hkv))
+    kc, vc = (torch.full((84, Hkv, page, d), 9.0, dtype=BF, device="cuda") for _ in range(2))
+    gtab = tab.cuda()
+    dims = dsa.make_dims(S, B, Hq, Hkv, d, page, max_pages, 1, 84, gtab)
+    wq, wk = (x.cuda() if norm else None for x in w)
+    rope = dsa.Rope(inv, rot, interleaved=inter, eps=1e-6, q_norm=wq, k_norm=wk)
+    ws = dsa.Workspace(dsa.WORKSPACE_HEADER_BYTES)
+    dsa.dsa_qk_norm_rope(q, k, v, qo, ko, vo, dims=dims, rope=rope, n_ctx=n.cuda(), workspace=ws,
+                         n_new=torch.tensor(new, dtype=torch.int32, device="cuda"), k_cache=kc, v_cache=vc)
+    assert ws.status() == dsa.DSA_OK
+    cq, ck, cv = views(qkv, S, B, Hq, Hkv, d)
+    pos = n[:, None] + torch.arange(B)
+    for got, x, wt, what in ((qo, cq, w[0], "q"), (ko, ck, w[1], "k")):
+        y, size = plain.norm_rope(x, wt if norm else None, pos, inv.cpu(), rot, inter, 1.0, 1e-6)
+        for s in range(S):
+            check(got[s, :new[s]], (y[s, :new[s]], size[s, :new[s]]), what)
+            assert (got[s, new[s]:] == 7.0).all()
+    slots = torch.zeros(84, page, dtype=torch.bool)
+    for s in range(S):
+        assert torch.equal(vo[s, :new[s]].cpu(), cv[s, :new[s]])
+        at = int(n[s]) + torch.arange(new[s])
+        pages, inside = tab[s, at // page].long(), at % page
+        slots[pages, inside] = True
+        assert torch.equal(kc.cpu()[pages, :, inside], ko[s, :new[s]].cpu())
+        assert torch.equal(vc.cpu()[pages, :, inside], cv[s, :new[s]])
+    assert (kc.cpu().transpose(1, 2)[~slots] == 9.0).all() and (vc.cpu().transpose(1, 2)[~slots] == 9.0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("page", [16, 32, 64])
 @pytest.mark.parametrize("both", [False, True])
 def test_append_padded_batch(lib, page, both):
