@@ -7,13 +7,16 @@ namespace {
 
 constexpr int kKv4Threads = 256;
 
-// Scale of a group whose largest magnitude is amax: the smallest number of five
-// significant bits that is at least amax / 7.  A true division: a product with 1/7
-// would push exact multiples of 7 over their border.
-__device__ __forceinline__ float kv4_scale(float amax) {
-  if (!(amax < 1.329227996e36f)) return __int_as_float(0x7fc00000);  // 2^120 or more, or NaN
-  if (amax < 7.888609052e-31f) return 0.f;                           // 2^-100
-  return __uint_as_float((__float_as_uint(__fdiv_rn(amax, 7.f)) + 0x7ffffu) & ~0x7ffffu);
+// Scale of a group whose largest magnitude has the bits amax (bf16): the smallest number of
+// five significant bits that is at least amax / 7, 0 below 2^-100, NaN from 2^120 on (and for
+// NaN).  The product with a seventh less 2^-20 of it stands for the division: with amax = A 2^e,
+// A of eight bits, a quotient that is no five-bit number lies at least 1/255 above the border
+// below it, and one that is falls under its border by less than rounding up puts back.
+__device__ __forceinline__ float kv4_scale(uint32_t amax) {
+  if (amax >= 0x7b80u) return __int_as_float(0x7fc00000);
+  if (amax < 0x0d80u) return 0.f;
+  constexpr float kSeventh = (1.f - 1.f / 1048576.f) / 7.f;
+  return __uint_as_float((__float_as_uint(__uint_as_float(amax << 16) * kSeventh) + 0x7ffffu) & ~0x7ffffu);
 }
 
 // Walks a CTA's rows (token, K | V, head), kRows apart: TT tokens from t0, found once per
@@ -89,42 +92,31 @@ __global__ void __launch_bounds__(kKv4Threads)
     const int i = at.i, r = at.r;
     at.step();
     load();
-    float x[8];
-    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&raw);
+    // magnitudes order as their bits do, infinities and NaN above all numbers
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t big = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+    big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const float s = kv4_scale(max(big >> 16, big & 0xffffu));
+    // Nearest integer to x / s, ties to even, without a division each.  x / s is half way between
+    // integers or at least 2^-9 off (x has eight significant bits, s five, |x| <= 7 s), so
+    // rounding the product with 1/s (two units off at most) to a multiple of 2^-11 first meets
+    // the half-way quotients exactly and moves no other across.  The next sum rounds that to an
+    // integer; four codes are then the digits of one fp32 integer, eight a word.
+    const float inv = __fdividef(1.f, s);
+    constexpr float kTo11 = 6144.f, kTo0 = 12582912.f;  // 1.5 2^12, 1.5 2^23: a unit is 2^-11, 1
+    float2 digits = make_float2(kTo0 + 34952.f, kTo0 + 34952.f);  // 8 (1 + 16 + 256 + 4096)
+    float place = 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(p[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+      const float2 y = sm100::fma2(x, make_float2(inv, inv), make_float2(kTo11, kTo11));
+      const float2 m = sm100::add2(sm100::add2(y, make_float2(kTo0 - kTo11, kTo0 - kTo11)), make_float2(-kTo0, -kTo0));
+      digits = sm100::fma2(m, make_float2(place, place), digits);
+      place *= 16.f;
     }
-    float amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = fmaxf(amax, fabsf(x[i]));
-      bad |= x[i] != x[i];
-    }
-    if (bad) amax = INFINITY;  // fmaxf drops NaN
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const float s = kv4_scale(amax);
-    uint32_t w = 0x88888888u;
-    if (s > 0.f) {
-      // Nearest integer to x / s, ties to even, without a division each.  2 x / s differs from
-      // an integer m >= 1 by nothing or by at least 2^-8 (x has eight significant bits, s five,
-      // x <= 7 s), so a product within 2^-10 of m stands for m itself, and a half-way quotient
-      // is met exactly.  The sum with 1.5 * 2^23 + 8 rounds to an integer, ties to even, and
-      // leaves the code in the low bits.
-      const float inv = __fdiv_rn(2.f, s);
-      constexpr float kMagic = 12582912.f;
-      w = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = x[i] * inv, m = __fadd_rn(__fadd_rn(y, kMagic), -kMagic);
-        const float z = fabsf(y - m) < 0.0009765625f ? m : y;
-        w |= (__float_as_uint(__fmaf_rn(z, 0.5f, kMagic + 8.f)) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
-      }
-    }
+    uint32_t w = __byte_perm(__float_as_uint(digits.x), __float_as_uint(digits.y), 0x5410);
+    if (!(s > 0.f)) w = 0x88888888u;
     if (i >= TT || rows[i] < 0) continue;
     const bool isv = r >= sh.Hkv;
     const long long row = rows[i] + (isv ? r - sh.Hkv : r) * sh.P;

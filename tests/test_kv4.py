@@ -94,6 +94,61 @@ def test_store_and_load(lib, S, B, Hkv, d, page, n, new):
 
 
 @pytest.mark.gpu
+def test_all_significands(lib):
+    """Every significand of a value under every significand of its group's largest, six exponents
+    down, against the definition in integers."""
+    g = torch.Generator().manual_seed(4)
+    a = torch.arange(128, 256).double()
+    x = (a[:, None] * torch.exp2(-torch.arange(6).double())).reshape(-1)  # 768 values
+    x = torch.cat([x, x[:7]]).view(25, 31).expand(128, 25, 31)
+    x = torch.where(x > a[:, None, None], x / 2, x) * torch.where(torch.rand(128, 25, 31, generator=g) < 0.5, -1, 1)
+    x = torch.cat([a[:, None, None].expand(128, 25, 1), x], -1) * torch.exp2(torch.randint(-60, 60, (128, 25, 1), generator=g).double())
+    x = x.reshape(1, 800, 2, 64).to(BF)
+    dims = dsa.make_dims(1, 800, 2, 2, 64, 16, 50, 1, 50)
+    cache = dsa.Kv4Cache.zeros(50, 2, 16, 64)
+    ws = dsa.Workspace(dsa.WORKSPACE_HEADER_BYTES)
+    dsa.dsa_kv4_store(x.cuda(), -x.cuda(), cache, dims=dims, n_ctx=torch.zeros(1, dtype=torch.int32, device="cuda"), workspace=ws)
+    assert ws.status() == dsa.DSA_OK
+    for y, codes, scales in ((x, cache.k, cache.k_scale), (-x, cache.v, cache.v_scale)):
+        c, s = plain.kv4_pack(y)
+        assert torch.equal(codes.cpu().transpose(1, 2).reshape(1, 800, 2, 32), c)
+        assert torch.equal(scales.cpu().transpose(1, 2).reshape(1, 800, 2, 2), s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv,d", [(1, 128), (3, 64)])
+def test_many_tokens_as_in_small_calls(lib, Hkv, d):
+    """A long padded batch, which takes several tokens a block of threads, leaves what calls of a
+    few hundred tokens leave, in the cache and on the way out."""
+    S, B, page, part = 3, 4001, 16, 667
+    x = torch.randn(S, B, Hkv, d, generator=torch.Generator().manual_seed(5)).to(BF).cuda()
+    n, new = [5, 0, 99], [B, 1, 3990]
+    max_pages = -(-(max(n) + B) // page)
+    table = torch.randperm(S * max_pages, generator=torch.Generator().manual_seed(6)).view(S, -1).to(torch.int32).cuda()
+    caches, outs = [], []
+    for step in (B, part):
+        cache = dsa.Kv4Cache.zeros(S * max_pages, Hkv, page, d)
+        out = torch.full((2, S, B, Hkv, d), 5.0, dtype=BF, device="cuda")
+        ws = dsa.Workspace(dsa.WORKSPACE_HEADER_BYTES)
+        for b in range(0, B, step):
+            m = min(step, B - b)
+            dims = dsa.make_dims(S, m, Hkv, Hkv, d, page, max_pages, 1, S * max_pages, table)
+            at = torch.tensor([i + b for i in n], dtype=torch.int32, device="cuda")
+            live = torch.tensor([min(max(i - b, 0), m) for i in new], dtype=torch.int32, device="cuda")
+            y = x[:, b:b + m].contiguous()
+            dsa.dsa_kv4_store(y, -y, cache, dims=dims, n_ctx=at, workspace=ws, n_new=live)
+            o = torch.full((2, S, m, Hkv, d), 5.0, dtype=BF, device="cuda")
+            dsa.dsa_kv4_load(cache, o[0], o[1], dims=dims, start=at, workspace=ws, n_new=live)
+            out[:, :, b:b + m] = o
+        assert ws.status() == dsa.DSA_OK
+        caches.append(cache)
+        outs.append(out)
+    a, b = caches
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v) and torch.equal(a.k_scale, b.k_scale) and torch.equal(a.v_scale, b.v_scale)
+    assert torch.equal(*outs) and (outs[0][:, 1, 1:] == 5.0).all() and (outs[0][:, 2, 3990:] == 5.0).all()
+
+
+@pytest.mark.gpu
 def test_bad_pages_are_skipped_and_reported(lib):
     S, B, Hkv, d, page = 1, 8, 2, 64, 16
     x = torch.randn(S, B, Hkv, d, generator=torch.Generator().manual_seed(0)).to(BF).cuda()
