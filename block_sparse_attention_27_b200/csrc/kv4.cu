@@ -1,5 +1,5 @@
 // kv4.cu -- dsa_kv4_store and dsa_kv4_load: rows into and out of the 4-bit cache.
-// Four lanes hold a group of 32 values, eight each: one packed word per lane.
+// Four lanes hold a group of 32 values, eight each: one packed word per lane and group.
 #include "paged.cuh"
 
 namespace dsa {
@@ -19,12 +19,44 @@ __device__ __forceinline__ float kv4_scale(uint32_t amax) {
   return __uint_as_float((__float_as_uint(__uint_as_float(amax << 16) * kSeventh) + 0x7ffffu) & ~0x7ffffu);
 }
 
-// Walks a CTA's rows (token, K | V, head), kRows apart: TT tokens from t0, found once per
+// Word of codes and scale of a lane's eight values; the four lanes of a group come together.
+__device__ __forceinline__ uint32_t kv4_codes(const uint4 &x, float &s) {
+  // magnitudes order as their bits do, infinities and NaN above all numbers
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t big = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+  big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  s = kv4_scale(max(big >> 16, big & 0xffffu));
+  // Nearest integer to x / s, ties to even, without a division each.  x / s is half way between
+  // integers or at least 2^-9 off (x has eight significant bits, s five, |x| <= 7 s), so
+  // rounding the product with 1/s (two units off at most) to a multiple of 2^-11 first meets
+  // the half-way quotients exactly and moves no other across.  The next sum rounds that to an
+  // integer; four codes are then the digits of one fp32 integer, eight a word.
+  const float inv = __fdividef(1.f, s);
+  constexpr float kTo11 = 6144.f, kTo0 = 12582912.f;  // 1.5 2^12, 1.5 2^23: a unit is 2^-11, 1
+  float2 digits = make_float2(kTo0 + 34952.f, kTo0 + 34952.f);  // 8 (1 + 16 + 256 + 4096)
+  float place = 1.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 z = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+    const float2 y = sm100::fma2(z, make_float2(inv, inv), make_float2(kTo11, kTo11));
+    const float2 m = sm100::add2(sm100::add2(y, make_float2(kTo0 - kTo11, kTo0 - kTo11)), make_float2(-kTo0, -kTo0));
+    digits = sm100::fma2(m, make_float2(place, place), digits);
+    place *= 16.f;
+  }
+  const uint32_t w = __byte_perm(__float_as_uint(digits.x), __float_as_uint(digits.y), 0x5410);
+  return s > 0.f ? w : 0x88888888u;
+}
+
+// Walks a CTA's rows (token, K | V, head), kPass apart: TT tokens from t0, found once per
 // token and kept in shared memory (looked up by every lane, they were most of the
-// instructions that bound these kernels: 284 and 165 a lane and row).
-template <int D, int TT>
+// instructions that bound these kernels: 284 and 165 a lane and row).  A lane holds C chunks of
+// eight values, kLanes chunks apart: four lanes a group, whole sectors a load, and what a row
+// costs besides is shared by twice the values.  32K tokens of 8 heads, store and load: 87 us, 73 without
+// a division and with packed arithmetic, 61 with two chunks a lane (the floor is 44).
+template <int D, int C>
 struct Rows {
-  static constexpr int kLanes = D / 8, kPass = kKv4Threads / kLanes;
+  static constexpr int kLanes = D / (8 * C), kPass = kKv4Threads / kLanes;
   int i, r, n, di, dr;  // token of the CTA, row of it, rows of a token; the step of one pass
   __device__ __forceinline__ Rows(int n_) : n(n_) {
     const int row = threadIdx.x / kLanes;
@@ -66,103 +98,114 @@ __device__ __forceinline__ void find_tokens(const Shape &sh, long long t0, const
   __syncthreads();
 }
 
-template <int D, int TT>
-__global__ void __launch_bounds__(kKv4Threads)
-    kv4_store(const Shape sh, const Kv4 c, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
+template <int D, int TT, int C>
+__global__ void __launch_bounds__(kKv4Threads, 8)
+    kv4_store(const Shape sh, const Kv4 c4, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
               const int32_t *__restrict__ n_ctx, const int32_t *__restrict__ n_new, uint32_t *status) {
   __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
   const long long t0 = (long long)blockIdx.x * TT;
   find_tokens<TT>(sh, t0, n_ctx, n_new, status, rows);
-  Rows<D, TT> at(2 * sh.Hkv);
-  const int l = threadIdx.x % Rows<D, TT>::kLanes;
-  uint4 next = make_uint4(0, 0, 0, 0);
+  Rows<D, C> at(2 * sh.Hkv);
+  constexpr int kLanes = Rows<D, C>::kLanes;
+  const int l = threadIdx.x % kLanes;
+  uint4 next[C];
   auto load = [&]() {
-    next = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < C; ++c) next[c] = make_uint4(0, 0, 0, 0);
     if (at.i >= TT || rows[at.i] < 0) return;
     const bool isv = at.r >= sh.Hkv;
-    next = __ldg(reinterpret_cast<const uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + (isv ? at.r - sh.Hkv : at.r)) * D) + l);
+    const uint4 *src = reinterpret_cast<const uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + (isv ? at.r - sh.Hkv : at.r)) * D) + l;
+#pragma unroll
+    for (int c = 0; c < C; ++c) next[c] = __ldg(src + c * kLanes);
   };
   load();
   // whole warps go round: a group's maximum is a shuffle
 #pragma unroll 1
-  for (int done = 0; done < TT * 2 * sh.Hkv; done += Rows<D, TT>::kPass) {
-    const uint4 raw = next;
+  for (int done = 0; done < TT * 2 * sh.Hkv; done += Rows<D, C>::kPass) {
+    uint4 raw[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) raw[c] = next[c];
     const int i = at.i, r = at.r;
     at.step();
     load();
-    // magnitudes order as their bits do, infinities and NaN above all numbers
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t big = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
-    big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const float s = kv4_scale(max(big >> 16, big & 0xffffu));
-    // Nearest integer to x / s, ties to even, without a division each.  x / s is half way between
-    // integers or at least 2^-9 off (x has eight significant bits, s five, |x| <= 7 s), so
-    // rounding the product with 1/s (two units off at most) to a multiple of 2^-11 first meets
-    // the half-way quotients exactly and moves no other across.  The next sum rounds that to an
-    // integer; four codes are then the digits of one fp32 integer, eight a word.
-    const float inv = __fdividef(1.f, s);
-    constexpr float kTo11 = 6144.f, kTo0 = 12582912.f;  // 1.5 2^12, 1.5 2^23: a unit is 2^-11, 1
-    float2 digits = make_float2(kTo0 + 34952.f, kTo0 + 34952.f);  // 8 (1 + 16 + 256 + 4096)
-    float place = 1.f;
+    uint32_t w[C];
+    float sc[C];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
-      const float2 y = sm100::fma2(x, make_float2(inv, inv), make_float2(kTo11, kTo11));
-      const float2 m = sm100::add2(sm100::add2(y, make_float2(kTo0 - kTo11, kTo0 - kTo11)), make_float2(-kTo0, -kTo0));
-      digits = sm100::fma2(m, make_float2(place, place), digits);
-      place *= 16.f;
-    }
-    uint32_t w = __byte_perm(__float_as_uint(digits.x), __float_as_uint(digits.y), 0x5410);
-    if (!(s > 0.f)) w = 0x88888888u;
+    for (int c = 0; c < C; ++c) w[c] = kv4_codes(raw[c], sc[c]);
     if (i >= TT || rows[i] < 0) continue;
     const bool isv = r >= sh.Hkv;
     const long long row = rows[i] + (isv ? r - sh.Hkv : r) * sh.P;
-    *reinterpret_cast<uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l) = w;
-    if (l % 4 == 0) (isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4] = __float2bfloat16_rn(s);
+    uint8_t *codes = (isv ? c4.v : c4.k) + row * (D / 2) + 4 * l;
+    __nv_bfloat16 *scales = (isv ? c4.vs : c4.ks) + row * (D / kKv4Group) + l / 4;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      *reinterpret_cast<uint32_t *>(codes + c * 4 * kLanes) = w[c];
+      if (l % 4 == 0) scales[c * (kLanes / 4)] = __float2bfloat16_rn(sc[c]);
+    }
   }
 }
 
-template <int D, int TT>
-__global__ void __launch_bounds__(kKv4Threads)
-    kv4_load(const Shape sh, const Kv4 c, __nv_bfloat16 *__restrict__ k, __nv_bfloat16 *__restrict__ v,
+template <int D, int TT, int C>
+__global__ void __launch_bounds__(kKv4Threads, 8)
+    kv4_load(const Shape sh, const Kv4 c4, __nv_bfloat16 *__restrict__ k, __nv_bfloat16 *__restrict__ v,
              const int32_t *__restrict__ start, const int32_t *__restrict__ n_new, uint32_t *status) {
   __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
   const long long t0 = (long long)blockIdx.x * TT;
   find_tokens<TT>(sh, t0, start, n_new, status, rows);
-  Rows<D, TT> at(2 * sh.Hkv);
-  const int l = threadIdx.x % Rows<D, TT>::kLanes;
+  Rows<D, C> at(2 * sh.Hkv);
+  constexpr int kLanes = Rows<D, C>::kLanes;
+  const int l = threadIdx.x % kLanes;
 #pragma unroll 4
   for (; at.i < TT; at.step()) {
     if (rows[at.i] < 0) continue;
     const bool isv = at.r >= sh.Hkv;
     const int h = isv ? at.r - sh.Hkv : at.r;
     const long long row = rows[at.i] + h * sh.P;
-    const uint32_t w = *reinterpret_cast<const uint32_t *>((isv ? c.v : c.k) + row * (D / 2) + 4 * l);
-    __nv_bfloat162 s8, m24;
-    kv4_constants((isv ? c.vs : c.ks)[row * (D / kKv4Group) + l / 4], s8, m24);
-    *reinterpret_cast<uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + h) * D + 8 * l) =
-        make_uint4(kv4_pair(w, 0, s8, m24), kv4_pair(w, 1, s8, m24), kv4_pair(w, 2, s8, m24), kv4_pair(w, 3, s8, m24));
+    const uint8_t *codes = (isv ? c4.v : c4.k) + row * (D / 2) + 4 * l;
+    const __nv_bfloat16 *scales = (isv ? c4.vs : c4.ks) + row * (D / kKv4Group) + l / 4;
+    __nv_bfloat16 *out = (isv ? v : k) + ((t0 + at.i) * sh.Hkv + h) * D + 8 * l;
+    uint32_t w[C];
+    __nv_bfloat16 sc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      w[c] = __ldg(reinterpret_cast<const uint32_t *>(codes + c * 4 * kLanes));
+      sc[c] = __ldg(scales + c * (kLanes / 4));
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      __nv_bfloat162 s8, m24;
+      kv4_constants(sc[c], s8, m24);
+      *reinterpret_cast<uint4 *>(out + c * 8 * kLanes) = make_uint4(kv4_pair(w[c], 0, s8, m24), kv4_pair(w[c], 1, s8, m24),
+                                                                    kv4_pair(w[c], 2, s8, m24), kv4_pair(w[c], 3, s8, m24));
+    }
   }
 }
 
 unsigned tokens_grid(const Shape &sh, int per) { return (unsigned)(((long long)sh.S * sh.B + per - 1) / per); }
-// Sixteen tokens a CTA once they still give every SM four CTAs, else one.
-constexpr int kTokens = 16;
-bool many_tokens(const Shape &sh) { return tokens_grid(sh, kTokens) >= 4u * 148u; }
+
+// A token a CTA and eight values a lane while that is quicker, then four tokens, and eight once
+// they fill the SMs (8 KV heads, store and load): 512 tokens 5.4, 6.1, 8.3 us; 2048 tokens 11.0, 8.3,
+// 9.6; 8192 tokens 33, 19.6, 20.3; 32766 tokens 136, 70.8, 67.6 (and 70.2 with sixteen).
+int tokens_per_cta(const Shape &sh) {
+  const long long tokens = (long long)sh.S * sh.B;
+  return tokens >= 8 * 8 * 148 ? 8 : tokens >= 1024 ? 4 : 1;
+}
 
 }  // namespace
 
-#define DSA_KV4_LAUNCH(kern, ...)                                                                                      \
-  if (many_tokens(sh))                                                                                                 \
-    return sh.d == 128 ? launch_pdl(kern<128, kTokens>, dim3(tokens_grid(sh, kTokens)), kKv4Threads, 0, stream, __VA_ARGS__) \
-                       : launch_pdl(kern<64, kTokens>, dim3(tokens_grid(sh, kTokens)), kKv4Threads, 0, stream, __VA_ARGS__); \
-  return sh.d == 128 ? launch_pdl(kern<128, 1>, dim3(tokens_grid(sh, 1)), kKv4Threads, 0, stream, __VA_ARGS__)          \
-                     : launch_pdl(kern<64, 1>, dim3(tokens_grid(sh, 1)), kKv4Threads, 0, stream, __VA_ARGS__)
+#define DSA_KV4_LAUNCH_D(kern, d, ...)                                                                        \
+  switch (tokens_per_cta(sh)) {                                                                               \
+    case 8: return launch_pdl(kern<d, 8, 2>, dim3(tokens_grid(sh, 8)), kKv4Threads, 0, stream, __VA_ARGS__);  \
+    case 4: return launch_pdl(kern<d, 4, 2>, dim3(tokens_grid(sh, 4)), kKv4Threads, 0, stream, __VA_ARGS__);  \
+    default: return launch_pdl(kern<d, 1, 1>, dim3(tokens_grid(sh, 1)), kKv4Threads, 0, stream, __VA_ARGS__); \
+  }
+#define DSA_KV4_LAUNCH(kern, ...)                          \
+  if (sh.d == 128) DSA_KV4_LAUNCH_D(kern, 128, __VA_ARGS__) \
+  DSA_KV4_LAUNCH_D(kern, 64, __VA_ARGS__)
 
 cudaError_t launch_kv4_store(const Shape &sh, const Kv4 &c, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
                              const int32_t *n_ctx, const int32_t *n_new, uint32_t *status, cudaStream_t stream) {
