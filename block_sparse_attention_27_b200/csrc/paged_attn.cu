@@ -512,6 +512,13 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   //   stop_full, stop_empty (it)   three slots: the one of stop it + 3 is written after
   //                        every role has left stop it.  The issuer reads stop it + 2 at most
   //                        while PV of stop it, which others wait for, is still to be sent.
+  // No role waits for what follows its own step.  PV(k) is sent after S(k + 2), so with stops of
+  // one tile PV of stop it needs K of stop it + 2, and nothing of stop it + 3: that one is
+  // written when stop it has been left, which its PV comes before.  So a loader must not hold
+  // back a tile while it waits for a stop: copied tiles are announced one tile late, but
+  // the last of a stop before the loader waits for the next (a table entry, a tile by TMA or a
+  // 4-bit tile is announced in its own step).  Within a stop, K(k - 1) is announced once S(k - ST)
+  // is done and V(k - 1) once PV(k - ST) is: both come before the S and PV that need them.
   if (KV4 ? warp == 0 : warp == 11) {
     // ------------------------------------------------- the walk, and queries --
     if (lane == 0) {
@@ -826,6 +833,12 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
     const uint32_t ring = base + (isv ? C::kOffV : C::kOffK);
     int k = 0, told = 0;  // tiles issued; tiles announced (copies by threads are, one tile late)
     bool ok = true;
+    auto announce_last = [&]() {
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(full((k - 1) % ST));
+      told = k;
+    };
     for (int it = 0; ok && __all_sync(0xffffffffu, arrive_at(it)); leave(it), ++it) {
       const Stop<KV4, PAGE> &at = *stop_at(it);
       const Keys &ks = at.ks;
@@ -908,14 +921,11 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
         lp = lp1;
         phys = phys1;
       }
+      // The next stop may not come before the MMAs on this one's last tile: unless it is there,
+      // that tile is announced now.
+      if (!kBoxes && ok && told < k && !__all_sync(0xffffffffu, mbar_test(stop_full(it + 1), ((it + 1) / 3) & 1))) announce_last();
     }
-    if (!kBoxes) {
-      cp_async_wait<0>();
-      if (told < k) {
-        fence_proxy_async_smem();
-        mbar_arrive(full((k - 1) % ST));
-      }
-    }
+    if (!kBoxes && told < k) announce_last();
     // copies in flight land before the CTA's shared memory is released
     if (lane == 0)
       for (int j = max(0, k - ST); j < k; ++j) mbar_wait_short(full(j % ST), (j / ST) & 1, drain_ctx);
