@@ -211,7 +211,8 @@ __device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &f
     const int lb = max(0, first.lb);  // the lowest position that a window of the unit reaches
     ks.nsp = (min(min(a.sinks, ks.n), lb) + PAGE - 1) / PAGE;
     ks.wp0 = max(ks.nsp, lb / PAGE);
-    ks.npg = ks.nsp + max(0, np - ks.wp0);
+    // (a window that begins at or behind the prefix's end has no page, not the one it may end in)
+    ks.npg = ks.nsp + (lb < ks.n ? max(0, np - ks.wp0) : 0);
     const int ue = a.blk_k ? (a.causal ? min(ks.nb, b_end) : ks.nb) : 0;
     ks.ua = max(0, min(ue, clamp_int((long long)last.sk - ks.n)));  // sinks that reach into the block
     ks.ub0 = max(ks.ua, clamp_int((long long)first.lb - ks.n));
