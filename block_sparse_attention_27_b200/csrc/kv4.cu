@@ -53,7 +53,8 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint4 &x, float &s) {
 // instructions that bound these kernels: 284 and 165 a lane and row).  A lane holds C chunks of
 // eight values, kLanes chunks apart: four lanes a group, whole sectors a load, and what a row
 // costs besides is shared by twice the values.  32K tokens of 8 heads, store and load: 87 us, 73 without
-// a division and with packed arithmetic, 61 with two chunks a lane (the floor is 44).
+// a division and with packed arithmetic, 61 with two chunks a lane, 59.5 with two rows' loads ahead of
+// their stores in the load (the floor is 44).
 template <int D, int C>
 struct Rows {
   static constexpr int kLanes = D / (8 * C), kPass = kKv4Threads / kLanes;
@@ -76,8 +77,8 @@ struct Rows {
 };
 // Row of head 0 in the cache of each of the CTA's tokens (head h is h * P further), -1: none.
 template <int TT>
-__device__ __forceinline__ void find_tokens(const Shape &sh, long long t0, const int32_t *__restrict__ first,
-                                            const int32_t *__restrict__ n_new, uint32_t *status, long long (&rows)[TT]) {
+__device__ __forceinline__ void find_tokens(const Shape &sh, long long t0, const int32_t *first,
+                                            const int32_t *n_new, uint32_t *status, long long (&rows)[TT]) {
   if (threadIdx.x < TT) {
     const long long t = t0 + threadIdx.x;
     long long row = -1;
@@ -100,8 +101,8 @@ __device__ __forceinline__ void find_tokens(const Shape &sh, long long t0, const
 
 template <int D, int TT, int C>
 __global__ void __launch_bounds__(kKv4Threads, 8)
-    kv4_store(const Shape sh, const Kv4 c4, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
-              const int32_t *__restrict__ n_ctx, const int32_t *__restrict__ n_new, uint32_t *status) {
+    kv4_store(const Shape sh, const Kv4 c4, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
+              const int32_t *n_ctx, const int32_t *n_new, uint32_t *status) {
   __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kKv4Threads, 8)
     const bool isv = at.r >= sh.Hkv;
     const uint4 *src = reinterpret_cast<const uint4 *>((isv ? v : k) + ((t0 + at.i) * sh.Hkv + (isv ? at.r - sh.Hkv : at.r)) * D) + l;
 #pragma unroll
-    for (int c = 0; c < C; ++c) next[c] = __ldg(src + c * kLanes);
+    for (int c = 0; c < C; ++c) next[c] = src[c * kLanes];
   };
   load();
   // whole warps go round: a group's maximum is a shuffle
@@ -149,38 +150,53 @@ __global__ void __launch_bounds__(kKv4Threads, 8)
 
 template <int D, int TT, int C>
 __global__ void __launch_bounds__(kKv4Threads, 8)
-    kv4_load(const Shape sh, const Kv4 c4, __nv_bfloat16 *__restrict__ k, __nv_bfloat16 *__restrict__ v,
-             const int32_t *__restrict__ start, const int32_t *__restrict__ n_new, uint32_t *status) {
+    kv4_load(const Shape sh, const Kv4 c4, __nv_bfloat16 *k, __nv_bfloat16 *v, const int32_t *start,
+             const int32_t *n_new, uint32_t *status) {
   __shared__ long long rows[TT];
   sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
   const long long t0 = (long long)blockIdx.x * TT;
   find_tokens<TT>(sh, t0, start, n_new, status, rows);
   Rows<D, C> at(2 * sh.Hkv);
-  constexpr int kLanes = Rows<D, C>::kLanes;
+  constexpr int kLanes = Rows<D, C>::kLanes, kAhead = 2;
   const int l = threadIdx.x % kLanes;
-#pragma unroll 4
-  for (; at.i < TT; at.step()) {
-    if (rows[at.i] < 0) continue;
-    const bool isv = at.r >= sh.Hkv;
-    const int h = isv ? at.r - sh.Hkv : at.r;
-    const long long row = rows[at.i] + h * sh.P;
-    const uint8_t *codes = (isv ? c4.v : c4.k) + row * (D / 2) + 4 * l;
-    const __nv_bfloat16 *scales = (isv ? c4.vs : c4.ks) + row * (D / kKv4Group) + l / 4;
-    __nv_bfloat16 *out = (isv ? v : k) + ((t0 + at.i) * sh.Hkv + h) * D + 8 * l;
-    uint32_t w[C];
-    __nv_bfloat16 sc[C];
+  // Rows kAhead at a time: their loads go out before the first store, behind which the next rows'
+  // loads stay.  64K tokens of 4 heads: 25.5 us; three rows 29.2, four 29.7 (no more registers with
+  // six CTAs an SM: 29.2 and 29.6).
+#pragma unroll 1
+  while (at.i < TT) {
+    uint32_t w[kAhead][C];
+    __nv_bfloat16 sc[kAhead][C];
+    __nv_bfloat16 *out[kAhead];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      w[c] = __ldg(reinterpret_cast<const uint32_t *>(codes + c * 4 * kLanes));
-      sc[c] = __ldg(scales + c * (kLanes / 4));
+    for (int u = 0; u < kAhead; ++u) {
+      out[u] = nullptr;
+      if (at.i < TT && rows[at.i] >= 0) {
+        const bool isv = at.r >= sh.Hkv;
+        const int h = isv ? at.r - sh.Hkv : at.r;
+        const long long row = rows[at.i] + h * sh.P;
+        const uint8_t *codes = (isv ? c4.v : c4.k) + row * (D / 2) + 4 * l;
+        const __nv_bfloat16 *scales = (isv ? c4.vs : c4.ks) + row * (D / kKv4Group) + l / 4;
+        out[u] = (isv ? v : k) + ((t0 + at.i) * sh.Hkv + h) * D + 8 * l;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          w[u][c] = *reinterpret_cast<const uint32_t *>(codes + c * 4 * kLanes);
+          sc[u][c] = scales[c * (kLanes / 4)];
+        }
+      }
+      at.step();
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      __nv_bfloat162 s8, m24;
-      kv4_constants(sc[c], s8, m24);
-      *reinterpret_cast<uint4 *>(out + c * 8 * kLanes) = make_uint4(kv4_pair(w[c], 0, s8, m24), kv4_pair(w[c], 1, s8, m24),
-                                                                    kv4_pair(w[c], 2, s8, m24), kv4_pair(w[c], 3, s8, m24));
+    for (int u = 0; u < kAhead; ++u) {
+      if (!out[u]) continue;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        __nv_bfloat162 s8, m24;
+        kv4_constants(sc[u][c], s8, m24);
+        *reinterpret_cast<uint4 *>(out[u] + c * 8 * kLanes) =
+            make_uint4(kv4_pair(w[u][c], 0, s8, m24), kv4_pair(w[u][c], 1, s8, m24), kv4_pair(w[u][c], 2, s8, m24),
+                       kv4_pair(w[u][c], 3, s8, m24));
+      }
     }
   }
 }
@@ -188,8 +204,8 @@ __global__ void __launch_bounds__(kKv4Threads, 8)
 unsigned tokens_grid(const Shape &sh, int per) { return (unsigned)(((long long)sh.S * sh.B + per - 1) / per); }
 
 // A token a CTA and eight values a lane while that is quicker, then four tokens, and eight once
-// they fill the SMs (8 KV heads, store and load): 512 tokens 5.4, 6.1, 8.3 us; 2048 tokens 11.0, 8.3,
-// 9.6; 8192 tokens 33, 19.6, 20.3; 32766 tokens 136, 70.8, 67.6 (and 70.2 with sixteen).
+// they fill the SMs (8 KV heads, store and load): 512 tokens 5.8, 6.0, 7.8 us; 1024 tokens 7.4, 6.6,
+// 7.8; 2048 tokens 11.4, 8.4, 9.1; 8192 tokens 35.6, 19.9, 20.2; 32766 tokens 142, 70.3, 65.9.
 int tokens_per_cta(const Shape &sh) {
   const long long tokens = (long long)sh.S * sh.B;
   return tokens >= 8 * 8 * 148 ? 8 : tokens >= 1024 ? 4 : 1;

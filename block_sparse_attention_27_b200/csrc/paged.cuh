@@ -1,5 +1,10 @@
 // paged.cuh -- what the operators beside the two passes share: the block's token
 // counts, the lookup of a logical token in the paged cache, the 4-bit code.
+//
+// These kernels are launched as programmatic dependents: their blocks are resident while the
+// kernel ahead still writes what they read after the dependency wait.  None of it is read-only
+// for their life, which the read-only path (__ldg, const __restrict__ parameters) asks for, so
+// every load here is a plain one.
 #pragma once
 
 #include <algorithm>

@@ -186,7 +186,7 @@ __device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &f
   ks.h = unit / prm.rowtiles % sh.Hkv;
   ks.s = unit / prm.rowtiles / sh.Hkv;
   ks.b0 = rt * prm.bpt;
-  ks.n = clamp_prefix(__ldg(a.n_ctx + ks.s), sh.max_pages, PAGE, a.status, report);
+  ks.n = clamp_prefix(a.n_ctx[ks.s], sh.max_pages, PAGE, a.status, report);
   ks.nb = block_tokens(a.n_new, ks.s, sh.B, a.status, report);
   const int b_end = min(ks.b0 + prm.bpt, ks.nb);  // the unit's tokens are [b0, b_end)
   ks.rows = max(0, b_end - ks.b0) * sh.G;
@@ -198,7 +198,7 @@ __device__ __forceinline__ Keys unit_keys(const Params &prm, int unit, Limits &f
     ks.wp0 = 0;
     ks.npg = np;
     if (a.idx) {
-      ks.npg = __ldg(a.idx_cnt + (size_t)ks.s * sh.Hkv + ks.h);
+      ks.npg = a.idx_cnt[(size_t)ks.s * sh.Hkv + ks.h];
       if (ks.npg < 0 || ks.npg > sh.kmax) {
         if (report) raise_status(a.status, kStatusBadIndex);
         ks.npg = max(0, min(ks.npg, sh.kmax));
@@ -247,7 +247,7 @@ struct Stop {
     phys = -1;
     if (t >= ks.pt || i >= ks.npg) return;
     if (KV4 && prm.a.idx) {
-      lp = __ldg(prm.a.idx + ((size_t)ks.s * sh.Hkv + ks.h) * sh.kmax + i);
+      lp = prm.a.idx[((size_t)ks.s * sh.Hkv + ks.h) * sh.kmax + i];
       if (lp < 0 || (long long)lp * PAGE >= ks.n) lp = -2;
     } else {
       lp = i < ks.nsp ? i : ks.wp0 + (i - ks.nsp);
@@ -1095,11 +1095,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 
 // 16 keys on their way into fragments.
 template <int D>
@@ -1112,7 +1107,7 @@ struct KeysBf16 {
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if ((on >> (g + 8 * i)) & 1u) x = ld_stream(reinterpret_cast<const uint4 *>(row + (g + 8 * i) * stride) + t + 4 * c);
+        if ((on >> (g + 8 * i)) & 1u) x = reinterpret_cast<const uint4 *>(row + (g + 8 * i) * stride)[t + 4 * c];
         k[i][4 * c] = x.x; k[i][4 * c + 1] = x.y; k[i][4 * c + 2] = x.z; k[i][4 * c + 3] = x.w;
       }
   }
@@ -1123,7 +1118,7 @@ struct KeysBf16 {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if ((on >> key) & 1u) x = ld_stream(reinterpret_cast<const uint4 *>(row + key * stride + (D / 8) * g) + c);
+        if ((on >> key) & 1u) x = reinterpret_cast<const uint4 *>(row + key * stride + (D / 8) * g)[c];
         v[i][4 * c] = x.x; v[i][4 * c + 1] = x.y; v[i][4 * c + 2] = x.z; v[i][4 * c + 3] = x.w;
       }
     }
