@@ -15,10 +15,11 @@ namespace {
 constexpr int kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads)
-    merge_attn(const __nv_bfloat16 *__restrict__ o_a, const float *__restrict__ lse_a,
-               const __nv_bfloat16 *__restrict__ o_b, const float *__restrict__ lse_b,
+    merge_attn(const __nv_bfloat16 *o_a, const float *lse_a, const __nv_bfloat16 *o_b, const float *lse_b,
                __nv_bfloat16 *o_out, float *lse_out, long long rows, int d) {
-  sm100::grid_dep_wait();  // the two results come from the kernels ahead
+  // The two results come from the kernels ahead, which may still write them while this block is
+  // resident, and o_out may be one of them: plain loads, after the wait.
+  sm100::grid_dep_wait();
   sm100::grid_dep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (kMergeThreads / 32);

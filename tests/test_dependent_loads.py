@@ -8,7 +8,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_attention_27_b200", "csrc")
-FILES = ["kv4.cu", "paged.cuh", "paged_attn.cu", "rope.cu"]
+FILES = ["kv4.cu", "merge.cu", "paged.cuh", "paged_attn.cu", "rope.cu"]
 
 
 def code(name):
