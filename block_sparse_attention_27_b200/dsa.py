@@ -532,12 +532,12 @@ def dsa_window_attn(q_blk, k_cache, v_cache, blk_k, blk_v, o_out, stream=None, *
 
 
 def _with_lse_out(dims: dsa_dims, lse_out, dev) -> dsa_dims:
-    """dims for one call with its log-sum-exp output: that of the argument, else none."""
+    """dims for one call with its log-sum-exp output: that of the argument, else none (an address
+    left in dims stands for a tensor that nobody has checked for this call)."""
     if lse_out is None and not dims.lse_out:
         return dims
     d = dsa_dims.from_buffer_copy(dims)
-    if lse_out is not None:
-        d.lse_out = _arg(lse_out, "lse_out", torch.float32, (dims.S, dims.B, dims.Hq), dev)
+    d.lse_out = _opt(lse_out, "lse_out", torch.float32, (dims.S, dims.B, dims.Hq), dev)
     return d
 
 
