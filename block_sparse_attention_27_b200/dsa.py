@@ -346,7 +346,10 @@ def dsa_merge_attn(o_a, lse_a, o_b, lse_b, o_out, lse_out=None, stream=None):
 
 
 # ------------------------------------------- operators beside the two passes ----
-_INT32_MAX = 2 ** 31 - 1  # a window or a count of sinks past it is past every position
+def _int32(x) -> int:
+    """A window or a count of sinks as 32 bits hold it: past them it is past every position, and one
+    below zero stays so (ctypes would keep the low bits)."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
 
 
 # A call's host time counts where its kernel takes a few microseconds: each tensor is checked
@@ -508,7 +511,7 @@ def window_workspace_size(dims: dsa_dims) -> int:
 
 def window_launches(dims: dsa_dims, window, sinks=0, causal=False) -> int:
     rc = int(load().dsa_window_launches(ctypes.byref(dims), ctypes.byref(dsa_window(
-        min(int(window), _INT32_MAX), min(int(sinks), _INT32_MAX), int(bool(causal)), None))))
+        _int32(window), _int32(sinks), int(bool(causal)), None))))
     if rc < 0:
         raise DsaError(rc, "dsa_window_launches")
     return rc
@@ -522,7 +525,7 @@ def dsa_window_attn(q_blk, k_cache, v_cache, blk_k, blk_v, o_out, stream=None, *
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
     bf, dev = torch.bfloat16, torch.cuda.current_device()
     cache, blk = (dims.n_phys, Hkv, dims.page, d), (S, B, Hkv, d)
-    w = dsa_window(min(int(window), _INT32_MAX), min(int(sinks), _INT32_MAX), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,), dev))
+    w = dsa_window(_int32(window), _int32(sinks), int(bool(causal)), _opt(n_new, "n_new", torch.int32, (S,), dev))
     dims = _with_lse_out(dims, lse_out, dev)
     _call(load().dsa_window_attn(
         _arg(q_blk, "q_blk", bf, (S, B, Hq, d), dev), _arg(k_cache, "k_cache", bf, cache, dev),
