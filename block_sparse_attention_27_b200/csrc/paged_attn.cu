@@ -1672,8 +1672,11 @@ PagedPlan make_plan(const Shape &sh, int sms, long long max_tiles, bool kv4) {
   const int per_sm = !p.few ? 1 : kv4 ? (g.rows <= 8 ? FewCfg<128, true, 1>::kPerSm : FewCfg<128, true, 2>::kPerSm)
                                       : FewCfg<128, false, 1>::kPerSm;
   const int ctas = per_sm * sms;
-  // whole units where there are many, or where none is long enough to be cut
-  p.shared_out = g.units <= std::min((long long)kManyUnits * ctas, (long long)kMaxShared) && max_tiles > kMinTiles;
+  // Whole units where there are many, or where none is long enough to be cut, or where the tiles
+  // of all, which the CTAs count in 32 bits, could be too many (a unit's ranges may each end in
+  // a tile that max_tiles does not count).
+  p.shared_out = g.units <= std::min((long long)kManyUnits * ctas, (long long)kMaxShared) && max_tiles > kMinTiles &&
+                 g.units * (max_tiles + 4) <= INT_MAX;
   p.ctas = p.shared_out ? ctas : (int)std::min<long long>(ctas, g.units);
   p.launches = p.shared_out && ctas > 1 ? 2 : 1;
   // the same for every window, so that one workspace serves a model's layers
