@@ -405,9 +405,10 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, device="cuda"):
       None
       ("linear", f)      every position divided by f
       ("ntk", f)         the base raised so that the slowest pair is stretched f times
-      ("yarn", f, n0)    pairs that turn more than 32 times within the trained length n0 are
-                         kept, those that turn less than once are stretched f times, a linear
-                         ramp over the pair index between; cos and sin times 0.1 ln f + 1
+      ("yarn", f, n0)    the method of that name (Peng et al., 2023): pairs that turn more than 32
+                         times within the trained length n0 are kept, those that turn less than
+                         once are stretched f times, a linear ramp over the pair index between
+                         (its ends rounded outwards); cos and sin times 0.1 ln f + 1
     """
     if rot < 8 or rot % 8:
         raise ValueError("rot must be a positive multiple of 8")
@@ -430,7 +431,7 @@ def rope_inv_freq(rot, base=10000.0, *, scaling=None, device="cuda"):
                 return rot * math.log(n0 / (turns * 2 * math.pi)) / (2 * math.log(base))
 
             lo = max(0.0, float(math.floor(pair(32.0))))
-            hi = min(rot / 2 - 1.0, float(math.ceil(pair(1.0))))
+            hi = min(rot - 1.0, float(math.ceil(pair(1.0))))  # (past the last pair if all turn more than once)
             ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
             freq = freq * (1 - ramp) + freq / f * ramp
             scale = 0.1 * math.log(f) + 1.0

@@ -31,3 +31,27 @@ def test_integers_below_32_bits_are_refused(lib, window, sinks):
     with pytest.raises(dsa.DsaError) as e:
         dsa.window_launches(dims, window, sinks)
     assert e.value.code == dsa.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("rot,base,n0", [(128, 1e4, 131072), (64, 1e4, 262144), (128, 1e4, 4096), (128, 1e6, 32768), (64, 5e5, 8192),
+                                         (8, 100.0, 4096)])
+def test_yarn_ramp(rot, base, n0):
+    """Against the method's definition, also where every pair turns more than once within n0: there the
+    ramp ends behind the last pair, which is stretched in part only."""
+    f = 4.0
+    got, scale = dsa.rope_inv_freq(rot, base, scaling=("yarn", f, n0), device="cpu")
+    turns = [n0 * base ** (-2 * i / rot) / (2 * math.pi) for i in range(rot // 2)]
+
+    def at(t):  # the pair index, not whole, that turns t times
+        return rot / 2 * math.log(n0 / (2 * math.pi * t)) / math.log(base)
+
+    lo, hi = max(0, math.floor(at(32))), min(rot - 1, math.ceil(at(1)))
+    for i, x in enumerate(got.tolist()):
+        ramp = min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3)))
+        want = base ** (-2 * i / rot) * (1 - ramp + ramp / f)
+        assert abs(x - want) <= 2.0 ** -23 * want, (i, x, want)  # one rounding to fp32, and 64-bit arithmetic
+        if turns[i] > 32 and hi > lo:
+            assert ramp == 0
+        if 1 < turns[i]:
+            assert ramp < 1 or hi - lo < 1
+    assert scale == 0.1 * math.log(f) + 1
