@@ -397,7 +397,7 @@ int dsa_qk_norm_rope(const void *q, const void *k, const void *v, void *q_out, v
 size_t dsa_window_workspace_size(const dsa_dims *dims) {
   Shape sh;
   if (make_shape(dims, &sh, true) != DSA_OK || sh.G > 128) return 0;
-  // the longest reach needs the most splits' room: no window is cut shorter than the prefix
+  // one size for every window, sinks and causal: room for each CTA's two pieces
   return dsa::plan_window(sh, num_sms_current(), INT32_MAX, 0).total;
 }
 

@@ -44,8 +44,18 @@ constexpr int kNever = INT_MAX;  // position of a key that takes no part
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kTabs = 8;        // tiles whose positions are kept: six are in flight at most
 constexpr int kMinTiles = 1;    // least tiles of a share
-constexpr int kManyUnits = 8;   // units per CTA from which shares are whole units
-constexpr int kMaxShared = 1536;  // most units that are cut into equal shares
+// Whole units from kManyUnits per CTA on, and above kMaxShared; equal shares of all tiles below.
+// Shares against whole units, us, 8 KV heads of 4 query heads:
+//   one token each over 4-bit prefixes of 1K to 8K: 16 sequences 47, 76; 64: 150, 194; 192: 407,
+//     458; 193: 410, 492; 256: 537, 577; 400: 833, 834; all of 4K: 64: 125, 130; 193: 351, 345;
+//     400: 709, 704
+//   one token each through a window of 4096 over 700 to 8K: 64: 149, 159; 193: 424, 446; 400: 870, 832
+//   32 tokens each over 4-bit prefixes of 300 to 4K: 8: 47, 83; 32: 151, 148; 74: 191, 144; 147: 443,
+//     377; 193: 570, 520; through a window of 1024: 32: 73, 46; 147: 209, 161; 300: 361, 326
+// So shares pay for ragged single tokens until far more units than these limits let through, and
+// for blocks only while units are fewer than CTAs, or their lengths differ widely.
+constexpr int kManyUnits = 8;
+constexpr int kMaxShared = 1536;
 
 // A wait in few instructions (these kernels have many, and code that outgrows the
 // instruction cache costs them at every tile): a short spin in place, the bounded wait in
@@ -1125,8 +1135,6 @@ struct KeysBf16 {
   }
   // first element of the four of a lane in step j of the contraction
   static __device__ __forceinline__ int k_at(int t, int j) { return (t + 4 * (j >> 1)) * 8 + 4 * (j & 1); }
-  __device__ __forceinline__ void k_begin() {}
-  __device__ __forceinline__ void v_begin(uint32_t) {}
   __device__ __forceinline__ void k_frag(int j, uint32_t (&a)[4]) const {
     a[0] = k[0][2 * j]; a[1] = k[1][2 * j]; a[2] = k[0][2 * j + 1]; a[3] = k[1][2 * j + 1];
   }
