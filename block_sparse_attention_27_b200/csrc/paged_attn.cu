@@ -507,6 +507,11 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
   //   k_full, v_full (k)   the stage's next fill follows k_empty / v_empty of tile k,
   //                        committed after the MMAs that follow the issuer's wait.  Softmax
   //                        threads wait for v_full(k) before P(k), which PV(k) follows.
+  //                        The fill before is done: the issuer waited for it, and a softmax
+  //                        thread, which has S(k), knows PV(k - 3) done, so V(k - 3) and what
+  //                        was before it.  With two stages (4-bit cache) the fill before
+  //                        is V(k - 2), which may be missing still: there it waits for
+  //                        PV(k - 2) first, which needs nothing of tile k but S(k).
   //   k_empty, v_empty     a stage's next commit needs the fill that follows the wait.
   //   tab_full (k)         slot k's next fill is tile k + 8; its loader has waited for S of
   //                        tile k + 8 - ST, k + 3 at the least, which needs PV(k), so P(k).
@@ -670,20 +675,25 @@ __global__ void __launch_bounds__(Cfg<D, KV4>::kThreads, 1)
                   if (i == w) bits[i] = b;
               }
             }
-            // value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O
-            alive = __all_sync(0xffffffffu, mbar_wait_short(v_full(st), (k / ST) & 1, ctx));
-            if (!alive) break;
+            // Value rows that no row of the unit sees are zeroed: 0 * stale data must not reach O.
+            // (In a 4-bit tile of pages they are zeros already.)
+            if (!KV4 || blk) {
+              // with fewer than three stages V(k - ST) may not be there yet: see v_full above
+              if (ST < 3 && k >= ST) alive = __all_sync(0xffffffffu, mbar_wait_short(pv_done(k - ST), ((k - ST) >> 1) & 1, ctx));
+              if (alive) alive = __all_sync(0xffffffffu, mbar_wait_short(v_full(st), (k / ST) & 1, ctx));
+              if (!alive) break;
 #pragma unroll 1
-            for (int key = quarter * 32 + lane; key < kBN; key += 32 * aw) {
-              const int from = blk ? tab[0] : tab[key / PAGE];
-              if (from != kNever && seen(from + (blk ? key : key % PAGE), end, all)) continue;
-              unsigned char *row = smem + C::kOffV + st * C::kTile + key * 128;
+              for (int key = quarter * 32 + lane; key < kBN; key += 32 * aw) {
+                const int from = blk ? tab[0] : tab[key / PAGE];
+                if (from != kNever && seen(from + (blk ? key : key % PAGE), end, all)) continue;
+                unsigned char *row = smem + C::kOffV + st * C::kTile + key * 128;
 #pragma unroll
-              for (int hf = 0; hf < C::kHalves; ++hf)
+                for (int hf = 0; hf < C::kHalves; ++hf)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + hf * C::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+                  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + hf * C::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
           }
           // The row's scores, all 128 in registers; with the 4-bit cache's warps beside it a
           // thread has 128 registers: it holds the first 64, and reads the others twice.

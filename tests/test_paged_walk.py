@@ -48,6 +48,31 @@ def test_the_model_shows_a_tile_held_back():
         assert not wm.stalls([[(COPY, True)], [(COPY, True)], [(TMA, True)]], stages, "late")
 
 
+def random_stops(rng):
+    return [[(rng.choice((COPY, TMA)), rng.random() < 0.4) for _ in range(rng.choice((1, 1, 2, 3, 4, 9)))]
+            for _ in range(rng.randint(1, 7))]
+
+
+def test_every_wait_names_its_own_phase():
+    """Roles of very different speeds: a wait by parity never meets a phase two away from its own
+    (Aliased).  With two stages a softmax group may reach tile k before V(k - 2) has come, so that
+    waiting for V(k) alone passes at once, and the rows it zeroes are V(k - 2)'s; three stages
+    need no more, since S(k) follows PV(k - 3)."""
+    for stages, announce in KINDS:
+        for seed in range(2000):
+            rng = random.Random(seed)
+            wm.Cta(random_stops(rng), stages, announce, rng).run()
+    met = 0
+    for seed in range(2000):
+        rng = random.Random(seed)
+        try:
+            wm.Cta(random_stops(rng), 2, "at once", rng, pv_first=False).run()
+        except wm.Aliased as e:
+            assert "v_full" in str(e)
+            met += 1
+    assert met > 20
+
+
 # the GPU tests' shapes (test_walks.py)
 @pytest.mark.parametrize("name", sorted(wm.WALKS))
 def test_calls_end(name):

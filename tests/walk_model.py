@@ -46,8 +46,10 @@ class Cta:
     """stops: a list of stops, each a list of (kind, masked) per tile; masked: the softmax group zeroes
     value rows, so it waits for V before it decides the tile."""
 
-    def __init__(self, stops, stages, announce, rng):
+    def __init__(self, stops, stages, announce, rng, pv_first=None):
         self.stops, self.st, self.announce, self.rng = stops, stages, announce, rng
+        # a softmax group that waits for V(k) waits for PV(k - stages) first
+        self.pv_first = stages < 3 if pv_first is None else pv_first
         bars = lambda name, n, count=1: [Bar(f"{name}[{i}]", count) for i in range(n)]  # noqa: E731
         self.k_full, self.k_empty = bars("k_full", stages), bars("k_empty", stages)
         self.v_full, self.v_empty = bars("v_full", stages), bars("v_empty", stages)
@@ -126,6 +128,8 @@ class Cta:
                 yield self.tab_full[k % 8], k // 8
                 yield self.s_full[k % 3], k // 3
                 if self.stops[it][k - k0][1]:
+                    if self.pv_first and k >= self.st:
+                        yield self.pv_done[(k - self.st) % 2], (k - self.st) // 2
                     yield self.v_full[k % self.st], k // self.st
                 if k > k0:
                     yield self.decided[(k - 1) % 2], (k - 1) // 2
@@ -176,19 +180,18 @@ class Cta:
         roles = [self.walk(), self.issuer(), self.softmax(0), self.softmax(1), self.loader(False), self.loader(True)]
         names = ["walk", "issuer", "softmax 0", "softmax 1", "K", "V"]
         live = [[n, r, None] for n, r in zip(names, roles)]
+        # some roles are slower than others by up to three powers of ten, so that each gets far ahead
+        speed = {n: 10.0 ** -self.rng.choice((0, 0, 1, 3)) for n in names}
         while live:
-            moved = False
-            for role in self.rng.sample(live, len(live)):
-                if role[2] is not None and not role[2][0].passed(role[2][1]):
-                    continue
-                moved = True
-                try:
-                    role[2] = next(role[1])
-                except StopIteration:
-                    live.remove(role)
-            if not moved:
+            ready = [r for r in live if r[2] is None or r[2][0].passed(r[2][1])]
+            if not ready:
                 tiles = sum(map(len, self.stops))
                 raise Stall(f"{self.pv} of {tiles} PVs; " + ", ".join(f"{n} at {w[0].name}" for n, _, w in live))
+            role = self.rng.choices(ready, [speed[r[0]] for r in ready])[0]
+            try:
+                role[2] = next(role[1])
+            except StopIteration:
+                live.remove(role)
         return self
 
 
