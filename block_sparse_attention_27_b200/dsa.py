@@ -612,7 +612,7 @@ def kv4_launches(dims: dsa_dims, sparse: bool) -> int:
 def dsa_kv4_attn(q_blk, cache: Kv4Cache, idx, blk_k, blk_v, o_out, stream=None, *, dims: dsa_dims,
                  n_ctx, workspace: Workspace, idx_cnt=None, n_new=None, lse_out=None):
     """The sparse pass over a 4-bit cache: the pages idx names, or every page where idx is None,
-    and the block's own tokens (see include/dsa.h)."""
+    and the block's own tokens (see include/dsa.h; dsa_select itself reads a bf16 cache only)."""
     S, B, Hq, Hkv, d = dims.S, dims.B, dims.Hq, dims.Hkv, dims.d
     bf, blk, dev = torch.bfloat16, (S, B, Hkv, d), torch.cuda.current_device()
     dims = _with_lse_out(dims, lse_out, dev)

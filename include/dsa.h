@@ -405,7 +405,10 @@ int dsa_kv4_load(const dsa_kv4 *cache, void *k_out, void *v_out, dsa_stream_t st
  * the pages idx[s, h, 0 .. idx_cnt-1] (rules of dsa_sparse_attn), or of every page where
  * idx and idx_cnt are NULL, and to the block's own n_new[s] tokens (bf16, no mask inside the
  * block; blk_k and blk_v both NULL: the prefix alone).  o_out and dims->lse_out as above; a
- * row without a key gets o = 0, lse = -inf.  B * Hq/Hkv <= 256.  dsa_kv4_launches() launches.
+ * row without a key gets o = 0, lse = -inf.  B * Hq/Hkv <= 256 and Hq/Hkv <= 128.
+ * dsa_kv4_launches() launches.  dsa_select reads a bf16 cache only, so idx comes from a
+ * prefix that is held in bf16 too (dsa_kv4_load gives the values of this cache in bf16), or from
+ * a selection of the caller's own.
  */
 int dsa_kv4_attn(const void *q_blk, const dsa_kv4 *cache, const int32_t *idx, const void *blk_k,
                  const void *blk_v, void *o_out, dsa_stream_t stream, const dsa_dims *dims,
