@@ -44,14 +44,14 @@ constexpr int kNever = INT_MAX;  // position of a key that takes no part
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kTabs = 8;        // tiles whose positions are kept: six are in flight at most
 constexpr int kMinTiles = 1;    // least tiles of a share
-// Whole units from kManyUnits per CTA on, and above kMaxShared; equal shares of all tiles below.
+// Whole units above kManyUnits per CTA and above kMaxShared in all; equal shares of all tiles below.
 // Shares against whole units, us, 8 KV heads of 4 query heads:
-//   one token each over 4-bit prefixes of 1K to 8K: 16 sequences 47, 76; 64: 150, 194; 192: 407,
-//     458; 193: 410, 492; 256: 537, 577; 400: 833, 834; all of 4K: 64: 125, 130; 193: 351, 345;
-//     400: 709, 704
-//   one token each through a window of 4096 over 700 to 8K: 64: 149, 159; 193: 424, 446; 400: 870, 832
-//   32 tokens each over 4-bit prefixes of 300 to 4K: 8: 47, 83; 32: 151, 148; 74: 191, 144; 147: 443,
-//     377; 193: 570, 520; through a window of 1024: 32: 73, 46; 147: 209, 161; 300: 361, 326
+//   one token each over 4-bit prefixes of 1K to 8K: 16 sequences 47, 76; 64: 150, 194; 192: 409,
+//     459; 193: 411, 494; 256: 537, 581; 400: 834, 835; all of 4K: 64: 126, 130; 193: 350, 345;
+//     400: 710, 705
+//   one token each through a window of 4096 over 700 to 8K: 64: 162, 170; 193: 458, 467; 400: 900, 872
+//   32 tokens each over 4-bit prefixes of 300 to 4K: 8: 45, 73; 32: 137, 139; 74: 187, 140; 147: 434,
+//     371; 193: 562, 514; through a window of 1024: 32: 74, 47; 147: 209, 161; 300: 362, 329
 // So shares pay for ragged single tokens until far more units than these limits let through, and
 // for blocks only while units are fewer than CTAs, or their lengths differ widely.
 constexpr int kManyUnits = 8;
